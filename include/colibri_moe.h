@@ -60,6 +60,22 @@
  * (v_mfma_scale_f32_32x32x64_f8f6f4, the scales applied as E8M0 exponents),
  * exact products summed in fp32. h stays bf16 and the down GEMM is the 8-bit
  * weight one. With stage timing, stage 1 includes the x quantization.
+ *
+ * 4-bit expert weights (COLIBRI_MOE_FLAG_MXFP4_WEIGHTS, bf16 layers): the same
+ * reading of the converter's narrow expert weights in the OCP microscaling
+ * format MXFP4: along a weight row, every block of 32 values holds E2M1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one E8M0 scale 2^e, the
+ * smallest power of two (e >= -127) with the block's largest magnitude at most
+ * 6 * 2^e (e = 0 for a block of zeros); code = w / 2^e rounded to the nearest
+ * E2M1 value, ties to even, zero keeping the sign. Forward computes the layer
+ * of the values the codes stand for, with bf16 activations and fp32
+ * accumulation, reading 17/64 of the bf16 layer's weight bytes.
+ *
+ * 4-bit activations (COLIBRI_MOE_FLAG_MXFP4_ACTIVATIONS, on top of
+ * MXFP4_WEIGHTS): each token row is quantized by the same rule for the gate/up
+ * GEMM (the router sees the full x), which multiplies 4-bit by 4-bit codes on
+ * v_mfma_scale_f32_32x32x64_f8f6f4. h stays bf16 for the down GEMM. With stage
+ * timing, stage 1 includes the x quantization.
  */
 #ifndef COLIBRI_MOE_H
 #define COLIBRI_MOE_H
@@ -78,7 +94,9 @@ typedef enum {
                                          max_tokens*k*d_ff, max_tokens*d_model or
                                          2*d_ff*d_model reaching 2^31, FP8_WEIGHTS with
                                          dtype F32, FP8_ACTIVATIONS without FP8_WEIGHTS
-                                         or with d_model or d_ff below 256 */
+                                         or with d_model or d_ff below 256, MXFP4_WEIGHTS
+                                         with dtype F32 or FP8_WEIGHTS,
+                                         MXFP4_ACTIVATIONS without MXFP4_WEIGHTS */
     COLIBRI_MOE_ERR_ALIGNMENT = 3,    /* x, y, a weight or topk_ids not 16-byte aligned, another
                                          routing buffer or b_router not 4-byte aligned */
     COLIBRI_MOE_ERR_OUT_OF_MEMORY = 4,/* init could not allocate its memory */
@@ -98,8 +116,12 @@ enum {
     COLIBRI_MOE_FLAG_STAGE_TIMING = 1u << 1, /* record per-stage GPU times (hipEvents) */
     COLIBRI_MOE_FLAG_FP8_WEIGHTS = 1u << 2,  /* bf16 only: keep expert weights as 8-bit codes
                                                 (format above) */
-    COLIBRI_MOE_FLAG_FP8_ACTIVATIONS = 1u << 3 /* with FP8_WEIGHTS, d_model and d_ff >= 256:
+    COLIBRI_MOE_FLAG_FP8_ACTIVATIONS = 1u << 3, /* with FP8_WEIGHTS, d_model and d_ff >= 256:
                                                   8-bit token rows, fp8 MFMA gate/up GEMM (above) */
+    COLIBRI_MOE_FLAG_MXFP4_WEIGHTS = 1u << 4,   /* bf16 only, without FP8_WEIGHTS: keep expert weights
+                                                   as 4-bit microscaled codes (above) */
+    COLIBRI_MOE_FLAG_MXFP4_ACTIVATIONS = 1u << 5 /* with MXFP4_WEIGHTS: 4-bit token rows, 4-bit MFMA
+                                                    gate/up GEMM (above) */
 };
 
 typedef struct {
@@ -185,6 +207,27 @@ colibri_moe_status_t colibri_moe_free(colibri_moe_t* h);
  * Needs no handle. */
 colibri_moe_status_t colibri_moe_quantize_fp8(const void* w, int64_t rows, int64_t cols, uint8_t* codes,
                                               float* scales, void* hip_stream);
+
+/* 4-bit microscaled codes of rows (the format above): w [rows][cols] bf16 or
+ * fp32, row r starting at element r * row_stride (row_stride >= cols), to codes
+ * [rows][cols/2] (value 2i of a row in the low half of byte i) and scales
+ * [rows][cols/32], one byte per 32 values. A block with a NaN or an infinity
+ * gets scale byte 255 (32 NaNs). Caller-owned DEVICE buffers, the codes 4-byte
+ * aligned, w aligned to its type. rows >= 1, cols a multiple of 32,
+ * rows * cols <= 2^40, rows * row_stride <= 2^42; otherwise INVALID_ARG.
+ * Enqueues on hip_stream (NULL = default stream) and returns without waiting.
+ * Needs no handle. */
+colibri_moe_status_t colibri_moe_quantize_mxfp4(const void* w, colibri_moe_dtype_t dtype, int64_t rows, int64_t cols,
+                                                int64_t row_stride, uint8_t* codes, uint8_t* scales, void* hip_stream);
+
+/* The values of 4-bit microscaled rows: out [rows][cols] bf16 or fp32, 16-byte
+ * aligned, code * 2^(scale - 127), exact in either type (products of 2^128 and
+ * more become infinities; quantize makes one of a value that rounds up to
+ * 2^128). Sizes, buffers and stream as above. A layer built from finite values
+ * read back this way holds the same values again, so weights that come in
+ * this format are given to init so. */
+colibri_moe_status_t colibri_moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                  int64_t cols, colibri_moe_dtype_t dtype, void* out, void* hip_stream);
 
 /* Measurement helper, not a step of the layer: copies `bytes` bytes from src
  * to dst (caller-owned DEVICE buffers, 16-byte aligned, not overlapping;

@@ -21,6 +21,8 @@ FLAG_ASYNC = 1 << 0
 FLAG_STAGE_TIMING = 1 << 1
 FLAG_FP8_WEIGHTS = 1 << 2
 FLAG_FP8_ACTIVATIONS = 1 << 3
+FLAG_MXFP4_WEIGHTS = 1 << 4
+FLAG_MXFP4_ACTIVATIONS = 1 << 5
 STAGES = ("router", "dispatch", "gate_up_gemm", "gate_up_reduce", "down_gemm", "combine")
 
 
@@ -43,7 +45,8 @@ class Routing(ctypes.Structure):
 
 EXPORTS = ("colibri_moe_init", "colibri_moe_forward", "colibri_moe_forward_static", "colibri_moe_free",
            "colibri_moe_status_string", "colibri_moe_stage_times", "colibri_moe_stage_name",
-           "colibri_moe_quantize_fp8", "colibri_moe_stream_copy")
+           "colibri_moe_quantize_fp8", "colibri_moe_quantize_mxfp4", "colibri_moe_dequantize_mxfp4",
+           "colibri_moe_stream_copy")
 
 _lib = None
 
@@ -73,6 +76,11 @@ def lib() -> ctypes.CDLL:
         L.colibri_moe_stage_name.argtypes = [i32]
         L.colibri_moe_quantize_fp8.restype = ctypes.c_int
         L.colibri_moe_quantize_fp8.argtypes = [P, ctypes.c_int64, ctypes.c_int64, P, P, P]
+        L.colibri_moe_quantize_mxfp4.restype = ctypes.c_int
+        L.colibri_moe_quantize_mxfp4.argtypes = [P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P,
+                                                 P]
+        L.colibri_moe_dequantize_mxfp4.restype = ctypes.c_int
+        L.colibri_moe_dequantize_mxfp4.argtypes = [P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P]
         L.colibri_moe_stream_copy.restype = ctypes.c_int
         L.colibri_moe_stream_copy.argtypes = [P, P, ctypes.c_int64, P]
         _lib = L
@@ -143,6 +151,72 @@ def quantize_fp8(w, stream=None):
     if st != OK:
         raise ColibriError("colibri_moe_quantize_fp8", st)
     return codes, scales
+
+
+def colibri_moe_quantize_mxfp4(w_ptr: int, dtype: int, rows: int, cols: int, row_stride: int, codes_ptr: int,
+                               scales_ptr: int, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_quantize_mxfp4(ctypes.c_void_p(w_ptr), dtype, rows, cols, row_stride,
+                                            ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr),
+                                            ctypes.c_void_p(hip_stream))
+
+
+def colibri_moe_dequantize_mxfp4(codes_ptr: int, scales_ptr: int, rows: int, cols: int, dtype: int, out_ptr: int,
+                                 hip_stream: int = 0) -> int:
+    return lib().colibri_moe_dequantize_mxfp4(ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr), rows, cols,
+                                              dtype, ctypes.c_void_p(out_ptr), ctypes.c_void_p(hip_stream))
+
+
+def quantize_mxfp4(w, stream=None):
+    """(codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]) of a 2-D
+    bf16 or fp32 device tensor whose rows are contiguous (they may be slices of
+    longer ones): the 4-bit microscaled codes a layer built with
+    FLAG_MXFP4_WEIGHTS keeps. cols must be a multiple of 32."""
+    import torch
+
+    if w.dtype not in (torch.bfloat16, torch.float32) or w.dim() != 2 or not w.is_cuda:
+        raise TypeError("w must be a 2-D bfloat16 or float32 device tensor")
+    rows, cols = w.shape
+    if cols % 32 != 0 or (cols > 1 and w.stride(1) != 1) or (rows > 1 and w.stride(0) < cols):
+        raise ValueError("rows must be contiguous, a multiple of 32 long, and must not overlap")
+    with torch.cuda.device(w.device):
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device=w.device)
+        if w.numel() == 0:
+            return codes, scales
+        s = stream if stream is not None else torch.cuda.current_stream()
+        st = colibri_moe_quantize_mxfp4(w.data_ptr(), BF16 if w.dtype == torch.bfloat16 else F32, rows, cols,
+                                        w.stride(0) if rows > 1 else cols, codes.data_ptr(), scales.data_ptr(),
+                                        s.cuda_stream)
+    if st != OK:
+        raise ColibriError("colibri_moe_quantize_mxfp4", st)
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
+    """The values [rows][cols] (bf16 by default, or fp32) of 4-bit microscaled
+    rows: contiguous uint8 device tensors codes [rows][cols/2] and scales
+    [rows][cols/32]. Exact."""
+    import torch
+
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    for t in (codes, scales):
+        if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+            raise TypeError("codes and scales must be contiguous 2-D uint8 device tensors")
+    rows, cols = codes.shape[0], codes.shape[1] * 2
+    if scales.device != codes.device or scales.shape[0] != rows or scales.shape[1] * 32 != cols:
+        raise ValueError("codes [rows][cols/2] and scales [rows][cols/32] do not belong together")
+    with torch.cuda.device(codes.device):
+        out = torch.empty(rows, cols, dtype=dtype, device=codes.device)
+        if out.numel() == 0:
+            return out
+        s = stream if stream is not None else torch.cuda.current_stream()
+        st = colibri_moe_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                          BF16 if dtype == torch.bfloat16 else F32, out.data_ptr(), s.cuda_stream)
+    if st != OK:
+        raise ColibriError("colibri_moe_dequantize_mxfp4", st)
+    return out
 
 
 def colibri_moe_stream_copy(src_ptr: int, dst_ptr: int, nbytes: int, hip_stream: int = 0) -> int:

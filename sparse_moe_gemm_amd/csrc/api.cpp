@@ -25,6 +25,7 @@ namespace {
 constexpr uint32_t kMagic = 0xC011B41Eu;
 constexpr int kStages = 6;
 constexpr int32_t kMaxTokensLimit = 1 << 24;
+constexpr size_t kMxBlockValues = 32;  // values per scale byte of the 4-bit format
 
 const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_up_gemm",
                                           "gate_up_reduce", "down_gemm", "combine"};
@@ -35,8 +36,9 @@ const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_u
 // buffers the caller did not supply, H, the fp32 partial sums, and the 8-bit
 // token rows of the W8A8 mode.
 struct Workspace {
-    uint8_t* xq;  // q8: token rows as E4M3 codes [T][d]
+    uint8_t* xq;  // q8: token rows as E4M3 codes [T][d]; q4: as E2M1 codes [T][d/2]
     float* xsc;   // q8: their scales by sorted position [A]
+    uint8_t* xsb; // q4: their scale bytes [T][d/32]
     float* topw;
     int32_t* ids;
     int32_t* counts;
@@ -65,8 +67,12 @@ struct colibri_moe {
     void* w_d;    // [E][d][f] (bf16: blocked MFMA layout; fp8: as w_gu)
     float* s_gu;  // fp8 row scales [E][2f] (interleaved rows), else null
     float* s_d;   // fp8 row scales [E][d], else null
+    uint8_t* m_gu;  // mx4: scale bytes of w_gu and w_d in the 4-bit GEMM layout
+    uint8_t* m_d;
     bool fp8;
     bool q8;      // 8-bit token rows for the gate/up GEMM too (fp8 MFMA)
+    bool mx4;     // 4-bit microscaled expert weights
+    bool q4;      // and token rows for the gate/up GEMM
     Workspace ws; // in the arena, sized for max_tokens
     int32_t* ccnt;  // fused combine: arrivals per token and 128-column tile [max_tokens][d/128], zero between calls
     bool timing;
@@ -184,6 +190,13 @@ colibri_moe_status_t validate_config(const colibri_moe_config_t* c)
     if ((c->flags & COLIBRI_MOE_FLAG_FP8_ACTIVATIONS) &&
         (!(c->flags & COLIBRI_MOE_FLAG_FP8_WEIGHTS) || c->d_model < 256 || c->d_ff < 256))
         return COLIBRI_MOE_ERR_UNSUPPORTED;
+    // 4-bit weights: bf16 layers, instead of 8-bit ones; 4-bit activations on
+    // top of them.
+    if ((c->flags & COLIBRI_MOE_FLAG_MXFP4_WEIGHTS) &&
+        (c->dtype != COLIBRI_MOE_BF16 || (c->flags & COLIBRI_MOE_FLAG_FP8_WEIGHTS)))
+        return COLIBRI_MOE_ERR_UNSUPPORTED;
+    if ((c->flags & COLIBRI_MOE_FLAG_MXFP4_ACTIVATIONS) && !(c->flags & COLIBRI_MOE_FLAG_MXFP4_WEIGHTS))
+        return COLIBRI_MOE_ERR_UNSUPPORTED;
     // GEMM source offsets are 32-bit element offsets.
     const int64_t lim = (int64_t)1 << 31;
     if ((int64_t)c->max_tokens * c->d_model >= lim || (int64_t)c->max_tokens * c->top_k * c->d_ff >= lim ||
@@ -219,8 +232,9 @@ size_t layout_workspace(const colibri_moe* h, int64_t T, bool up_to, uint8_t* ba
     const size_t d = c.d_model, f = c.d_ff, E = c.n_experts, k = c.top_k;
     const size_t A = (size_t)T * k;
     Carver cv;
-    const size_t o_xq = h->q8 ? cv.take((size_t)T * d) : 0;
+    const size_t o_xq = h->q8 ? cv.take((size_t)T * d) : h->q4 ? cv.take((size_t)T * d / 2) : 0;
     const size_t o_xsc = h->q8 ? cv.take(A * sizeof(float)) : 0;
+    const size_t o_xsb = h->q4 ? cv.take((size_t)T * d / kMxBlockValues) : 0;
     const size_t o_topw = cv.take(A * sizeof(float));
     const size_t o_ids = cv.take(A * sizeof(int32_t));
     const size_t o_cnt = cv.take(E * sizeof(int32_t));
@@ -241,8 +255,9 @@ size_t layout_workspace(const colibri_moe* h, int64_t T, bool up_to, uint8_t* ba
     }
     const size_t o_ys = cv.take(ys_floats * sizeof(float));
     if (base && ws) {
-        ws->xq = h->q8 ? base + o_xq : nullptr;
+        ws->xq = h->q8 || h->q4 ? base + o_xq : nullptr;
         ws->xsc = h->q8 ? (float*)(base + o_xsc) : nullptr;
+        ws->xsb = h->q4 ? base + o_xsb : nullptr;
         ws->topw = (float*)(base + o_topw);
         ws->ids = (int32_t*)(base + o_ids);
         ws->counts = (int32_t*)(base + o_cnt);
@@ -265,9 +280,11 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     Carver cv;
     const size_t o_wrt = cv.take(router_weight_bytes((int)d, (int)E, (int)es));
     const size_t o_br = cv.take(E * sizeof(float));
-    const size_t wes = h->fp8 ? 1 : es;  // bytes per stored expert weight
-    const size_t o_wgu = cv.take(E * 2 * f * d * wes);
-    const size_t o_wd = cv.take(E * d * f * wes);
+    const size_t wes = h->fp8 ? 1 : es;  // bytes per stored expert weight (mx4: below)
+    const size_t o_wgu = cv.take(h->mx4 ? mx_weight_bytes(E, 2 * f, d) : E * 2 * f * d * wes);
+    const size_t o_wd = cv.take(h->mx4 ? mx_weight_bytes(E, d, f) : E * d * f * wes);
+    const size_t o_mgu = h->mx4 ? cv.take(mx_weight_scale_bytes(E, 2 * f, d)) : 0;
+    const size_t o_md = h->mx4 ? cv.take(mx_weight_scale_bytes(E, d, f)) : 0;
     const size_t o_sgu = h->fp8 ? cv.take(E * 2 * f * sizeof(float)) : 0;
     const size_t o_sd = h->fp8 ? cv.take(E * d * sizeof(float)) : 0;
     const size_t o_ccnt = h->fuse_combine ? cv.take((size_t)c.max_tokens * (d / 128) * sizeof(int32_t)) : 0;
@@ -286,6 +303,8 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     h->w_d = base + o_wd;
     h->s_gu = h->fp8 ? (float*)(base + o_sgu) : nullptr;
     h->s_d = h->fp8 ? (float*)(base + o_sd) : nullptr;
+    h->m_gu = h->mx4 ? base + o_mgu : nullptr;
+    h->m_d = h->mx4 ? base + o_md : nullptr;
     h->ccnt = h->fuse_combine ? (int32_t*)(base + o_ccnt) : nullptr;
     layout_workspace(h, c.max_tokens, true, base + o_ws, &h->ws);
 
@@ -304,6 +323,10 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
         CMOE_HIP(launch_fp8_row_scales(w->w_down, nullptr, h->s_d, (int64_t)E * d, (int)d, (int)f, s));
         CMOE_HIP(launch_fp8_pack_blocked(w->w_gate, w->w_up, h->s_gu, h->w_gu, (int)E, (int)(2 * f), (int)d, s));
         CMOE_HIP(launch_fp8_pack_blocked(w->w_down, nullptr, h->s_d, h->w_d, (int)E, (int)d, (int)f, s));
+    } else if (h->mx4) {
+        // codes and scale bytes in the 4-bit GEMM layout
+        CMOE_HIP(launch_mx_pack_blocked(w->w_gate, w->w_up, h->w_gu, h->m_gu, (int)E, (int)(2 * f), (int)d, s));
+        CMOE_HIP(launch_mx_pack_blocked(w->w_down, nullptr, h->w_d, h->m_d, (int)E, (int)d, (int)f, s));
     } else if (c.dtype == COLIBRI_MOE_BF16) {
         // blocked MFMA operand layout (gate/up interleaved by 32 rows)
         CMOE_HIP(launch_pack_blocked(w->w_gate, w->w_up, h->w_gu, (int)E, (int)(2 * f), (int)d, 1, s));
@@ -348,6 +371,8 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     h->timing = (cfg->flags & COLIBRI_MOE_FLAG_STAGE_TIMING) != 0;
     h->fp8 = (cfg->flags & COLIBRI_MOE_FLAG_FP8_WEIGHTS) != 0;
     h->q8 = (cfg->flags & COLIBRI_MOE_FLAG_FP8_ACTIVATIONS) != 0;
+    h->mx4 = (cfg->flags & COLIBRI_MOE_FLAG_MXFP4_WEIGHTS) != 0;
+    h->q4 = (cfg->flags & COLIBRI_MOE_FLAG_MXFP4_ACTIVATIONS) != 0;
     // Tile order of the grouped GEMMs (tuning only; results do not depend
     // on it): n-tiles per group, CMOE_GROUP_N for both GEMMs.
     // Consecutive tiles go to the 8 XCDs in turn. With groups of 16 n-tiles
@@ -383,7 +408,7 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     // XCDs' separate L2s) and reads the other rows of a token with little
     // memory parallelism on the GEMM's critical path. Results are identical
     // either way.
-    h->fuse_combine = cfg->dtype == COLIBRI_MOE_BF16 && env_int("CMOE_FUSE_COMBINE", 0, 0, 1) != 0;
+    h->fuse_combine = cfg->dtype == COLIBRI_MOE_BF16 && !h->mx4 && env_int("CMOE_FUSE_COMBINE", 0, 0, 1) != 0;
     if (hipGetDevice(&h->device) != hipSuccess ||
         hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, h->device) != hipSuccess ||
         h->cus <= 0) {
@@ -404,18 +429,20 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     if (cfg->dtype == COLIBRI_MOE_BF16) {
         const int64_t amax = (int64_t)cfg->max_tokens * cfg->top_k;
         h->dec_max_a = (int)std::min<int64_t>(amax, env_int("CMOE_DECODE_MAX_A", 2048, 0, 1 << 16));
-        h->dec_gate_rows = env_int("CMOE_DECODE_MAX_ROWS", h->fp8 ? 32 : 48, 0, 1 << 16);
+        h->dec_gate_rows = env_int("CMOE_DECODE_MAX_ROWS", h->fp8 || h->mx4 ? 32 : 48, 0, 1 << 16);
         const int waves = cmoe::decode_waves(h->cus);
         // k step of the small-batch kernels: 16 (bf16 weights), 32 (8-bit
         // weights), 64 (8-bit token rows, gate/up only)
         const int kstep_dn = h->fp8 ? 32 : 16;
         const int kstep_gu = h->q8 ? 64 : kstep_dn;
-        h->dec_split_gu = cmoe::decode_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, kstep_gu, waves, 64);
+        h->dec_split_gu = h->mx4 ? cmoe::decode_mx_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, waves)
+                                 : cmoe::decode_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, kstep_gu, waves, 64);
         // No K slices: the gate/up items write H themselves (SiLU(g)*u in
         // their epilogue) instead of partials for a separate sum pass
         // (CMOE_DECODE_FUSE_SILU=0 keeps the pass)
         h->dec_fuse_silu = h->dec_split_gu == 1 && env_int("CMOE_DECODE_FUSE_SILU", 1, 0, 1) != 0;
-        h->dec_split_dn = cmoe::decode_split(cfg->n_experts, cfg->d_model, cfg->d_ff, kstep_dn, waves, 64);
+        h->dec_split_dn = h->mx4 ? cmoe::decode_mx_split(cfg->n_experts, cfg->d_model, cfg->d_ff, waves)
+                                 : cmoe::decode_split(cfg->n_experts, cfg->d_model, cfg->d_ff, kstep_dn, waves, 64);
     }
     st = init_impl(h, w);
     if (st != COLIBRI_MOE_OK) {
@@ -465,6 +492,9 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     const bool q8 = h->q8;
     if (q8)  // token rows to 8 bits, scales by sorted position
         CMOE_HIP(launch_act_quant(x, T, c.d_model, c.top_k, inv, ws.xq, ws.xsc, s));
+    const bool mx4 = h->mx4, q4 = h->q4;
+    if (q4)  // token rows to 4 bits
+        CMOE_HIP(launch_mx_quantize(x, 1, T, c.d_model, c.d_model, ws.xq, ws.xsb, s));
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[2], s));
 
@@ -480,7 +510,13 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     const int gate = small && h->dec_gate_rows > 0 && T > h->dec_gate_rows ? h->dec_gate_rows : 0;
     const bool tiled = !small || gate > 0;
     const bool order_m = (int64_t)A <= (int64_t)h->order_m_rows * c.n_experts;
-    if (small) {
+    const bool mx_small_tiles = (int64_t)A <= (int64_t)128 * c.n_experts;
+    if (small && mx4) {
+        MxDecodeArgs gu{q4 ? (const void*)ws.xq : x, q4 ? ws.xsb : nullptr, h->w_gu, h->m_gu, ws.Ys, offsets, perm,
+                        A, c.n_experts, c.d_model, c.d_ff, h->dec_split_gu,
+                        h->dec_fuse_silu ? (uint16_t*)ws.H : nullptr, gate};
+        CMOE_HIP(launch_decode_mx(gu, 1, h->cus, s));
+    } else if (small) {
         DecodeArgs gu{q8 ? (const void*)ws.xq : x, h->w_gu, h->s_gu, q8 ? ws.xsc : nullptr, ws.Ys, offsets, perm,
                       A, c.n_experts, c.d_model, c.d_ff, h->dec_split_gu};
         gu.h = h->dec_fuse_silu ? (uint16_t*)ws.H : nullptr;
@@ -488,7 +524,12 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
         gu.gate_rows = gate;
         CMOE_HIP(launch_decode_gemm(gu, 1, h->cus, s));
     }
-    if (tiled) {
+    if (tiled && mx4) {
+        MxGemmArgs gu{q4 ? (const void*)ws.xq : x, q4 ? ws.xsb : nullptr, h->w_gu, h->m_gu, ws.H, offsets, perm,
+                      A, c.n_experts, c.top_k, c.d_model, c.d_ff, order_m ? -8 : h->group_n_gu, 1, h->cus,
+                      mx_small_tiles ? 1 : 0, gate};
+        CMOE_HIP(launch_gate_up_mx(gu, s));
+    } else if (tiled) {
         GemmArgs gu{q8 ? (const void*)ws.xq : x, h->w_gu, h->s_gu, q8 ? ws.xsc : nullptr, ws.H, offsets, perm, A,
                     c.n_experts, c.top_k, c.d_model, c.d_ff, order_m ? -8 : h->group_n_gu, 1, h->cus};
         gu.xcd_map = h->xcd_map & 1;
@@ -512,7 +553,12 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     int split = 1;
     bool fused = false;    // combine done by the down GEMM
     int ys_bf16 = 0;       // expert outputs stored as bf16
-    if (small) {
+    if (small && mx4) {
+        MxDecodeArgs dn{ws.H, nullptr, h->w_d, h->m_d, ws.Ys, offsets, perm, A, c.n_experts, c.d_model, c.d_ff,
+                        h->dec_split_dn, nullptr, gate};
+        CMOE_HIP(launch_decode_mx(dn, 0, h->cus, s));
+        split = h->dec_split_dn;
+    } else if (small) {
         DecodeArgs dn{ws.H, h->w_d, h->s_d, nullptr, ws.Ys, offsets, perm,
                       A, c.n_experts, c.d_model, c.d_ff, h->dec_split_dn};
         dn.max_rows = T;
@@ -520,7 +566,12 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
         CMOE_HIP(launch_decode_gemm(dn, 0, h->cus, s));
         split = h->dec_split_dn;
     }
-    if (tiled) {
+    if (tiled && mx4) {
+        split = down_split_bf16(A, c.n_experts, c.d_model, c.d_ff, h->cus, 1);
+        MxGemmArgs dn{ws.H, nullptr, h->w_d, h->m_d, ws.Ys, offsets, perm, A, c.n_experts, c.top_k, c.d_model, c.d_ff,
+                      order_m ? -8 : h->group_n_dn, split, h->cus, mx_small_tiles ? 1 : 0, gate};
+        CMOE_HIP(launch_down_mx(dn, s));
+    } else if (tiled) {
         split = bf ? down_split_bf16(A, c.n_experts, c.d_model, c.d_ff, h->cus, 0) : 1;
         GemmArgs dn{ws.H, h->w_d, h->s_d, nullptr, ws.Ys, offsets, perm, A,
                     c.n_experts, c.top_k, c.d_model, c.d_ff, order_m ? -8 : h->group_n_dn, split, h->cus};
@@ -651,6 +702,32 @@ colibri_moe_status_t colibri_moe_quantize_fp8(const void* w, int64_t rows, int64
     CMOE_HIP(launch_fp8_row_scales(w, nullptr, scales, rows, 0, (int)cols, s));
     CMOE_HIP(launch_fp8_encode_rows(w, scales, codes, rows, (int)cols, s));
     CMOE_HIP(hipStreamSynchronize(s));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_quantize_mxfp4(const void* w, colibri_moe_dtype_t dtype, int64_t rows, int64_t cols,
+                                                int64_t row_stride, uint8_t* codes, uint8_t* scales, void* hip_stream)
+{
+    if (!w || !codes || !scales || rows < 1 || cols < 32 || cols % 32 != 0 || cols > INT32_MAX ||
+        rows > ((int64_t)1 << 40) / cols || row_stride < cols || row_stride > ((int64_t)1 << 42) / rows ||
+        (dtype != COLIBRI_MOE_BF16 && dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)w & (dtype == COLIBRI_MOE_BF16 ? 1u : 3u)) || ((uintptr_t)codes & 3u))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    CMOE_HIP(launch_mx_quantize(w, dtype == COLIBRI_MOE_BF16, rows, cols, row_stride, codes, scales,
+                                (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                  int64_t cols, colibri_moe_dtype_t dtype, void* out, void* hip_stream)
+{
+    if (!codes || !scales || !out || rows < 1 || cols < 32 || cols % 32 != 0 || cols > INT32_MAX ||
+        rows > ((int64_t)1 << 40) / cols || (dtype != COLIBRI_MOE_BF16 && dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)codes & 3u) || !aligned16(out))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    CMOE_HIP(launch_mx_dequantize(codes, scales, rows, cols, dtype == COLIBRI_MOE_BF16, out, (hipStream_t)hip_stream));
     return COLIBRI_MOE_OK;
 }
 

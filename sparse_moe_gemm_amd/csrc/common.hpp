@@ -213,6 +213,57 @@ hipError_t launch_act_quant(const void* x, int64_t rows, int cols, int k, const 
 hipError_t launch_fp8_encode_rows(const void* w, const float* scales, uint8_t* codes, int64_t rows, int cols,
                                   hipStream_t s);
 
+// 4-bit microscaled rows and weights (quant_mxfp4.hip; format and GEMM layout
+// in mxfp4.hpp). Codes [rows][cols/2] and scale bytes [rows][cols/32] of bf16
+// or fp32 rows (row r at w + r * ld elements), and back.
+hipError_t launch_mx_quantize(const void* w, int bf16_in, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int bf16_out,
+                                void* out, hipStream_t s);
+// bf16 expert weights [E][N][K] (w1: gate/up interleaved by 32 rows) in the
+// GEMM layout, and the sizes of its two parts.
+size_t mx_weight_bytes(int64_t E, int64_t N, int64_t K);
+size_t mx_weight_scale_bytes(int64_t E, int64_t N, int64_t K);
+hipError_t launch_mx_pack_blocked(const void* w0, const void* w1, void* out, uint8_t* scales, int E, int N, int K,
+                                  hipStream_t s);
+
+// Tiled grouped GEMMs on 4-bit weights (gemm_mxfp4.hip).
+struct MxGemmArgs {
+    const void* a;            // gate/up: x [T][d] bf16, or its codes; down: H [A][f] bf16
+    const uint8_t* a_scales;  // gate/up on 4-bit token rows: scale bytes [T][d/32]; else null
+    const void* b;            // weight codes and scales in the GEMM layout
+    const uint8_t* b_scales;
+    void* out;                // gate/up: H [A][f] bf16; down: fp32 partials [split][A][d]
+    const int32_t* offsets;   // [E+1]
+    const int32_t* perm;      // [A]
+    int A_max;                // A = T*k of this call
+    int E, k, d, f;
+    int group_n;              // tile order (tiles.hpp)
+    int split;                // K splits of the down GEMM
+    int cus;
+    int small_tiles;          // 1: tiles of 64 rows, 0: of 256
+    int skip_rows;            // as GemmArgs
+};
+hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s);
+hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s);
+
+// Small-batch GEMMs on 4-bit weights (decode_mxfp4.hip); fields as DecodeArgs.
+struct MxDecodeArgs {
+    const void* a;
+    const uint8_t* a_scales;  // gate/up on 4-bit token rows; else null
+    const void* b;
+    const uint8_t* b_scales;
+    float* part;
+    const int32_t* offsets;
+    const int32_t* perm;
+    int A, E, d, f;
+    int split;
+    uint16_t* h;
+    int gate_rows;
+};
+int decode_mx_split(int E, int N, int K, int waves);
+hipError_t launch_decode_mx(const MxDecodeArgs& a, int gate_up, int cus, hipStream_t s);
+
 struct CombineArgs {
     const float* ys;    // split partials, each [A][d] fp32 by sorted position (ys_bf16: one [A][d] bf16)
     const int32_t* inv; // [A]: sorted position of assignment t*k+j

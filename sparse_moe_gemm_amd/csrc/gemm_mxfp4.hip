@@ -1,0 +1,356 @@
+// gemm_mxfp4.hip - grouped expert GEMMs on 4-bit microscaled weights.
+//
+// The two expert GEMMs of gemm_bf16.hip for layers whose expert weights are
+// MXFP4 (mxfp4.hpp): for every sorted position p of expert e
+//   gate/up:  H[p][c]  = SiLU(sum_i X[perm[p]][i] Wg[e][c][i]) * (sum_i X[perm[p]][i] Wu[e][c][i])
+//   down:     Ys_s[p][o] = sum_{c in K split s} H[p][c] Wd[e][o][c]     (fp32)
+// with W the values the codes stand for. Two ways to multiply them:
+//   A4 false: bf16 rows (x for gate/up, H for down). A lane's 32 codes become
+//             four bf16 fragments in registers (exact) for
+//             v_mfma_f32_32x32x16_bf16.
+//   A4 true:  the token rows are MXFP4 too and gate/up runs on
+//             v_mfma_scale_f32_32x32x64_f8f6f4, 4-bit codes on both sides, one
+//             scale byte per lane: products of 4-bit values are multiples of
+//             1/4 up to 36, whose sums within a block are exact.
+// Both sum in fp32.
+//
+// A tile is BM sorted rows of one expert x 256 weight rows (x a K split); a
+// persistent workgroup walks its tiles (tiles.hpp) and streams their K stages
+// (64 k of bf16 rows, 128 k of 4-bit rows) through a ring of three LDS slots:
+// while stage s is multiplied, stage s + 1 has landed or is landing and stage
+// s + 2 is requested, across tile borders too. One wait and one barrier per
+// stage: after it every wave's loads of stage s are in LDS and every wave has
+// read stage s - 1 to the end, so its slot can take stage s + 2.
+// Waves form WAVES_M x 4; a wave multiplies WM = BM / WAVES_M rows with 64
+// weight rows (one gate and one up block of 32, so SiLU(g)*u stays in its
+// registers). The weight fragment is the MFMA's first operand: a result lane
+// holds one token row and groups of four consecutive outputs.
+#include "lds_dma.hpp"
+#include "mxfp4.hpp"
+#include "tiles.hpp"
+
+namespace cmoe {
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kBN = 256;   // weight rows per tile
+constexpr int kSlots = 3;  // LDS stages
+
+__device__ __forceinline__ float silu_fast(float z)
+{
+    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b)
+{
+    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+
+// One K stage: BM token rows of RB bytes (64 k as bf16, 128 k as codes), their
+// scale words (A4: bytes of the row's four blocks), KBS 1 KiB weight blocks
+// for each 32 weight rows and the scale group they belong to.
+template <int BM, bool A4>
+struct MxStage {
+    static constexpr int RB = A4 ? 64 : 128;
+    static constexpr int KBS = A4 ? 2 : 1;
+    Vec16 a[BM * RB / 16];
+    Vec16 b[(kBN / 32) * KBS * kWave];
+    uint32_t bs[(kBN / 32) * kWave];
+    uint32_t as[A4 ? BM : 1];
+};
+
+// Position of 16-byte chunk c of tile row r in the stage: the 16 rows that 16
+// lanes read at one chunk fall into 16 different 16-byte bank groups.
+template <bool A4>
+__device__ __forceinline__ int mx_swz(int r, int c)
+{
+    return A4 ? (c ^ ((r >> 2) & 3)) : (c ^ ((r >> 1) & 7));
+}
+
+template <int BM, int WAVES_M, bool A4>
+struct MxShape {
+    using Stage = MxStage<BM, A4>;
+    static constexpr int NW = WAVES_M * 4;
+    static constexpr int WM = BM / WAVES_M;
+    static constexpr int ROWS = A4 ? 16 : 8;            // tile rows per 1 KiB load
+    static constexpr int A_INS = BM / ROWS / NW;        // loads per wave and stage
+    static constexpr int B_INS = (kBN / 32) * Stage::KBS / NW;
+    static constexpr int S_INS = (kBN / 32) / NW;
+    static constexpr int NLD = A_INS + B_INS + S_INS + (A4 ? 1 : 0);
+    static_assert(A_INS >= 1 && B_INS >= 1 && S_INS >= 1, "every wave loads a share");
+};
+
+// Where the next stage to load comes from: a position in the stream of all K
+// stages of this workgroup's tiles.
+template <int A_INS>
+struct MxCursor {
+    Rsrc rb, rs;           // the tile's weight blocks and scale groups
+    uint32_t aoff[A_INS];  // byte offsets of this lane's rows and chunk
+    uint32_t asoff;        // A4: byte offset of this lane's row of scales
+    int kt, left;          // next stage along K, stages left in the tile
+    int L;                 // the tile's launch index
+};
+
+template <int BM, int WAVES_M, bool A4, bool GATE_UP>
+__global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx_gemm_kernel(
+    MxGemmArgs g)
+{
+    using Sh = MxShape<BM, WAVES_M, A4>;
+    using Stage = typename Sh::Stage;
+    constexpr int SM = GATE_UP ? 0 : 64;  // tile order as in the other GEMMs
+    constexpr int MI = Sh::WM / 32;
+    __shared__ Stage ring[kSlots];
+
+    const int N = GATE_UP ? 2 * g.f : g.d;
+    const int K = GATE_UP ? g.d : g.f;
+    const int NT = (N + kBN - 1) / kBN;
+    const int KB = K / 64, KG = mx_scale_groups(K);
+    const int KT = K / (A4 ? 128 : 64);
+    const int S = GATE_UP ? 1 : g.split;
+    const int lane = threadIdx.x % kWave;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wv / 4, wn = wv % 4;
+    const int half = lane >> 5;
+
+    TileTable tt;
+    const int total = make_table<BM, SM>(g.offsets, g.E, lane, NT * S, tt);
+    if (g.skip_rows > 0 && table_max_rows(tt) <= g.skip_rows)
+        return;  // the small-batch kernels take this call
+    const int GRID = gridDim.x;
+    if ((int)blockIdx.x >= total)
+        return;
+
+    const uint32_t Kbytes = A4 ? (uint32_t)K / 2 : (uint32_t)K * 2;
+    const uint32_t a_rows = GATE_UP ? (uint32_t)(g.A_max / g.k) : (uint32_t)g.A_max;
+    const Rsrc ra = buffer_rsrc(g.a, a_rows * Kbytes);
+    const Rsrc ras = buffer_rsrc(A4 ? (const void*)g.a_scales : g.a, A4 ? a_rows * (uint32_t)(K / 32) : 0u);
+    const uint32_t lane16 = (uint32_t)lane * 16u, lane4 = (uint32_t)lane * 4u;
+    const uint32_t ring0 = lds_address(&ring[0]);
+
+    auto row_of = [&](const Tile& t, int r) {
+        const int p = t.row0 + min(r, t.rows - 1);  // past the segment: its last row again
+        return (uint32_t)(GATE_UP ? g.perm[p] : p);
+    };
+    auto open = [&](MxCursor<Sh::A_INS>& c, int L) {
+        const Tile t = decode<BM, SM>(tt, L, NT, S, g.group_n, KT);
+        const int nb0 = t.n * (kBN / 32), nbs = N / 32 - nb0;  // row blocks from here to the expert's end
+        const int64_t blk = (int64_t)t.e * (N / 32) + nb0;
+        c.rb = buffer_rsrc((const uint8_t*)g.b + blk * KB * 1024, (uint32_t)min(nbs, kBN / 32) * (uint32_t)KB * 1024u);
+        c.rs = buffer_rsrc(g.b_scales + blk * KG * 256, (uint32_t)min(nbs, kBN / 32) * (uint32_t)KG * 256u);
+#pragma unroll
+        for (int q = 0; q < Sh::A_INS; ++q) {
+            const int per = Sh::Stage::RB / 16;  // chunks per row
+            const int r = (wv * Sh::A_INS + q) * Sh::ROWS + lane / per;
+            c.aoff[q] = row_of(t, r) * Kbytes + (uint32_t)mx_swz<A4>(r, lane % per) * 16u;
+        }
+        if constexpr (A4)
+            c.asoff = row_of(t, (wv % (BM / 64)) * 64 + lane) * (uint32_t)(K / 32);
+        c.kt = t.kt0;
+        c.left = t.nkt;
+        c.L = L;
+    };
+    // Requests the cursor's stage into slot `slot` and moves the cursor on;
+    // past the last tile it requests the last stage again (read by no one),
+    // which keeps the loads in flight per stage the same.
+    auto request = [&](MxCursor<Sh::A_INS>& c, int slot) {
+        const uint32_t base = ring0 + (uint32_t)slot * (uint32_t)sizeof(Stage);
+#pragma unroll
+        for (int q = 0; q < Sh::A_INS; ++q)
+            lds_load16(ra, c.aoff[q], (uint32_t)c.kt * (uint32_t)Stage::RB,
+                       base + (uint32_t)offsetof(Stage, a) + (uint32_t)(wv * Sh::A_INS + q) * 1024u);
+#pragma unroll
+        for (int q = 0; q < Sh::B_INS; ++q) {
+            const int i = wv * Sh::B_INS + q;  // row block i / KBS, k block i % KBS of the stage
+            lds_load16(c.rb, lane16,
+                       ((uint32_t)(i / Stage::KBS) * (uint32_t)KB + (uint32_t)(c.kt * Stage::KBS + i % Stage::KBS)) * 1024u,
+                       base + (uint32_t)offsetof(Stage, b) + (uint32_t)i * 1024u);
+        }
+#pragma unroll
+        for (int q = 0; q < Sh::S_INS; ++q) {
+            const int i = wv * Sh::S_INS + q;
+            lds_load4(c.rs, lane4, ((uint32_t)i * (uint32_t)KG + (uint32_t)(c.kt * Stage::KBS / 4)) * 256u,
+                      base + (uint32_t)offsetof(Stage, bs) + (uint32_t)i * 256u);
+        }
+        if constexpr (A4)
+            lds_load4(ras, c.asoff, (uint32_t)c.kt * 4u,
+                      base + (uint32_t)offsetof(Stage, as) + (uint32_t)(wv % (BM / 64)) * 256u);
+        if (c.left > 1) {
+            ++c.kt;
+            --c.left;
+        } else if (c.L + GRID < total) {
+            open(c, c.L + GRID);
+        }
+    };
+
+    MxCursor<Sh::A_INS> cur;
+    open(cur, blockIdx.x);
+    request(cur, 0);
+    request(cur, 1);
+    int slot = 0;
+
+    for (int L = blockIdx.x; L < total; L += GRID) {
+        const Tile t = decode<BM, SM>(tt, L, NT, S, g.group_n, KT);
+        floatx16 acc[2][MI];  // [gate/up or first/second 32 weight rows][32-row group]
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    acc[j][i][q] = 0.f;
+        const int wrows = t.rows - wm * Sh::WM;
+        const int RG = wrows <= 0 ? 0 : min((wrows + 31) / 32, MI);  // row groups with valid rows
+
+        // All K stages with the first RGC row groups multiplied.
+        auto stages = [&](auto rg_const) {
+            constexpr int RGC = decltype(rg_const)::value;
+            for (int j = 0; j < t.nkt; ++j) {
+                // (LDS reads too: the compiler may move the MFMAs that use them
+                // past the barrier, and their waits with them)
+                wait_vm<Sh::NLD>();
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                request(cur, slot == 0 ? 2 : slot - 1);
+                const Stage& st = ring[slot];
+                const int kb = (t.kt0 + j) * Stage::KBS;
+                if constexpr (RGC > 0) {
+                    if constexpr (A4) {
+                        uint32_t sb[2], sa[RGC];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            sb[n] = st.bs[(wn * 2 + n) * kWave + lane] >> (8 * (kb & 3));
+#pragma unroll
+                        for (int i = 0; i < RGC; ++i)
+                            sa[i] = st.as[wm * Sh::WM + i * 32 + (lane & 31)] >> (8 * half);
+                        auto step = [&](auto s_const) {
+                            constexpr int s = decltype(s_const)::value;
+                            v8i fb[2], fa[RGC];
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const Vec16 w = st.b[((wn * 2 + n) * 2 + s) * kWave + lane];
+                                fb[n] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                            }
+#pragma unroll
+                            for (int i = 0; i < RGC; ++i) {
+                                const int r = wm * Sh::WM + i * 32 + (lane & 31);
+                                const Vec16 w = st.a[r * 4 + mx_swz<true>(r, 2 * s + half)];
+                                fa[i] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                            }
+#pragma unroll
+                            for (int i = 0; i < RGC; ++i)
+#pragma unroll
+                                for (int n = 0; n < 2; ++n)
+                                    acc[n][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                        fb[n], fa[i], acc[n][i], 4, 4, s, (int)sb[n], 2 * s, (int)sa[i]);
+                        };
+                        step(std::integral_constant<int, 0>{});
+                        step(std::integral_constant<int, 1>{});
+                    } else {
+                        Vec16 wb[2];
+                        float sc[2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            wb[n] = st.b[(wn * 2 + n) * kWave + lane];
+                            sc[n] = mx_scale((st.bs[(wn * 2 + n) * kWave + lane] >> (8 * (kb & 3))) & 255u);
+                        }
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            bf16x8 fb[2], fa[RGC];
+#pragma unroll
+                            for (int i = 0; i < RGC; ++i) {
+                                const int r = wm * Sh::WM + i * 32 + (lane & 31);
+                                fa[i] = as_bf16x8(st.a[r * 8 + mx_swz<false>(r, 4 * half + s)]);
+                            }
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+                                fb[n] = mx8_to_bf16(wb[n][s], sc[n]);
+#pragma unroll
+                            for (int i = 0; i < RGC; ++i)
+#pragma unroll
+                                for (int n = 0; n < 2; ++n)
+                                    acc[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[i], acc[n][i], 0, 0, 0);
+                        }
+                    }
+                }
+                slot = slot == 2 ? 0 : slot + 1;
+            }
+        };
+        if (RG == MI)
+            stages(std::integral_constant<int, MI>{});
+        else if (MI > 2 && RG > 1)
+            stages(std::integral_constant<int, (MI > 2 ? MI - 1 : MI)>{});
+        else if (RG == 1)
+            stages(std::integral_constant<int, 1>{});
+        else
+            stages(std::integral_constant<int, 0>{});
+
+        // Outputs. Result lane: token row lane%32 of a 32-row group, weight rows
+        // 8 (q/4) + 4 (lane/32) + q%4.
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int row = wm * Sh::WM + i * 32 + (lane & 31);
+            if (row >= t.rows)
+                continue;
+            const int64_t p = t.row0 + row;
+            if constexpr (GATE_UP) {
+                uint16_t* hp = (uint16_t*)g.out + p * g.f + (t.n * kBN + wn * 64) / 2 + 4 * half;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    float h[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        h[q] = silu_fast(acc[0][i][4 * q4 + q]) * acc[1][i][4 * q4 + q];
+                    *(uint2*)(hp + 8 * q4) = make_uint2(bf16x2_bits(h[0], h[1]), bf16x2_bits(h[2], h[3]));
+                }
+            } else {
+                const int col0 = t.n * kBN + wn * 64;
+                float* yp = (float*)g.out + ((int64_t)t.s * g.A_max + p) * g.d + col0 + 4 * half;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (col0 + 32 * n >= N)  // a last tile of 128 weight rows
+                        continue;
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4)
+                        *(floatx4*)(yp + 32 * n + 8 * q4) = floatx4{acc[n][i][4 * q4], acc[n][i][4 * q4 + 1],
+                                                                    acc[n][i][4 * q4 + 2], acc[n][i][4 * q4 + 3]};
+                }
+            }
+        }
+    }
+    wait_vm<0>();  // the loads past the last tile
+}
+
+template <bool A4, bool GATE_UP>
+hipError_t launch_mx(const MxGemmArgs& a, hipStream_t s)
+{
+    const int N = GATE_UP ? 2 * a.f : a.d;
+    const int S = GATE_UP ? 1 : a.split;
+    const int NT = (N + kBN - 1) / kBN;
+    if (a.small_tiles) {
+        const int64_t bound = ((int64_t)a.A_max / 64 + a.E) * NT * S;
+        const int grid = (int)std::min<int64_t>(bound, 2 * a.cus);
+        hipLaunchKernelGGL((mx_gemm_kernel<64, 1, A4, GATE_UP>), dim3(grid), dim3(4 * kWave), 0, s, a);
+    } else {
+        const int64_t bound = ((int64_t)a.A_max / 256 + a.E) * NT * S;
+        const int grid = (int)std::min<int64_t>(bound, a.cus);
+        hipLaunchKernelGGL((mx_gemm_kernel<256, 2, A4, GATE_UP>), dim3(grid), dim3(8 * kWave), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s)
+{
+    return a.a_scales ? launch_mx<true, true>(a, s) : launch_mx<false, true>(a, s);
+}
+
+hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s)
+{
+    return launch_mx<false, false>(a, s);
+}
+
+}  // namespace cmoe
