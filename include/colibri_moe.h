@@ -102,12 +102,16 @@ typedef enum {
     COLIBRI_MOE_ERR_OUT_OF_MEMORY = 4,/* init could not allocate its memory */
     COLIBRI_MOE_ERR_HIP = 5,          /* a HIP launch, copy or sync failed */
     COLIBRI_MOE_ERR_TOO_LARGE = 6     /* colibri_moe_forward_static: the call's working memory
-                                         exceeds COLIBRI_MOE_STATIC_SCRATCH_BYTES */
+                                         exceeds COLIBRI_MOE_STATIC_SCRATCH_BYTES;
+                                         colibri_moe_forward_few: T > COLIBRI_MOE_FEW_TOKENS */
 } colibri_moe_status_t;
 
 /* Size of the static working-memory array of colibri_moe_forward_static, one
  * per GPU the library runs on (64 MiB). */
 #define COLIBRI_MOE_STATIC_SCRATCH_BYTES (64 << 20)
+
+/* Most tokens of a colibri_moe_forward_few call. */
+#define COLIBRI_MOE_FEW_TOKENS 16
 
 typedef enum { COLIBRI_MOE_F32 = 0, COLIBRI_MOE_BF16 = 1 } colibri_moe_dtype_t;
 
@@ -189,6 +193,22 @@ colibri_moe_status_t colibri_moe_forward(colibri_moe_t* h, const void* x, int32_
  * ERR_HIP if the array's device address could not be found at init. */
 colibri_moe_status_t colibri_moe_forward_static(colibri_moe_t* h, const void* x, int32_t T, void* y,
                                                 const colibri_moe_routing_t* routing_out);
+
+/* colibri_moe_forward for at most COLIBRI_MOE_FEW_TOKENS tokens, as when one or
+ * a few sequences generate, in two kernels: router, top-k and gate/up in one,
+ * down and combine in the other. A router whose weights are too large to be
+ * read by every workgroup (d_model * n_experts > 2^19, or more than 128
+ * experts) runs as a launch of its own before them. The same arguments and
+ * checks; every routing output is bit-identical to colibri_moe_forward's, and
+ * y is the same layer's to the rounding of its sums: fp32 throughout, h kept to
+ * 16 significant bits, only y rounded to bf16 (8-bit and 4-bit token rows meet
+ * the weights as the bf16 values they stand for). bf16 layers of any weight
+ * precision with d_ff at most 2^20; UNSUPPORTED otherwise, TOO_LARGE for more
+ * tokens. Uses the handle's memory: calls on one handle must not overlap.
+ * Allocates nothing. With stage timing, stage 0 is that separate router, stage 2
+ * the first kernel and stage 4 the second; the others are empty. */
+colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, int32_t T, void* y,
+                                             const colibri_moe_routing_t* routing_out);
 
 /* Release everything init allocated (waits for the handle's stream first).
  * NULL is a no-op. The library keeps a registry of live handles: forward and

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "libcolibri_moe.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_OUT_OF_MEMORY, ERR_HIP, ERR_TOO_LARGE = range(7)
 STATIC_SCRATCH_BYTES = 64 << 20  # COLIBRI_MOE_STATIC_SCRATCH_BYTES
+FEW_TOKENS = 16  # COLIBRI_MOE_FEW_TOKENS
 F32, BF16 = 0, 1
 FLAG_ASYNC = 1 << 0
 FLAG_STAGE_TIMING = 1 << 1
@@ -43,7 +44,8 @@ class Routing(ctypes.Structure):
                 ("perm", ctypes.c_void_p), ("perm_slot", ctypes.c_void_p), ("inv", ctypes.c_void_p)]
 
 
-EXPORTS = ("colibri_moe_init", "colibri_moe_forward", "colibri_moe_forward_static", "colibri_moe_free",
+EXPORTS = ("colibri_moe_init", "colibri_moe_forward", "colibri_moe_forward_static",
+           "colibri_moe_forward_few", "colibri_moe_free",
            "colibri_moe_status_string", "colibri_moe_stage_times", "colibri_moe_stage_name",
            "colibri_moe_quantize_fp8", "colibri_moe_quantize_mxfp4", "colibri_moe_dequantize_mxfp4",
            "colibri_moe_stream_copy")
@@ -66,6 +68,8 @@ def lib() -> ctypes.CDLL:
         L.colibri_moe_forward.argtypes = [P, P, i32, P, ctypes.POINTER(Routing)]
         L.colibri_moe_forward_static.restype = ctypes.c_int
         L.colibri_moe_forward_static.argtypes = [P, P, i32, P, ctypes.POINTER(Routing)]
+        L.colibri_moe_forward_few.restype = ctypes.c_int
+        L.colibri_moe_forward_few.argtypes = [P, P, i32, P, ctypes.POINTER(Routing)]
         L.colibri_moe_free.restype = ctypes.c_int
         L.colibri_moe_free.argtypes = [P]
         L.colibri_moe_status_string.restype = ctypes.c_char_p
@@ -106,6 +110,11 @@ def colibri_moe_forward_static(handle, x_ptr: int, T: int, y_ptr: int, routing: 
     return lib().colibri_moe_forward_static(ctypes.c_void_p(handle), ctypes.c_void_p(x_ptr), T,
                                             ctypes.c_void_p(y_ptr),
                                             None if routing is None else ctypes.byref(routing))
+
+
+def colibri_moe_forward_few(handle, x_ptr: int, T: int, y_ptr: int, routing: Routing | None = None) -> int:
+    return lib().colibri_moe_forward_few(ctypes.c_void_p(handle), ctypes.c_void_p(x_ptr), T, ctypes.c_void_p(y_ptr),
+                                         None if routing is None else ctypes.byref(routing))
 
 
 def colibri_moe_free(handle) -> int:
@@ -300,6 +309,14 @@ class MoELayer:
         routing outputs; missing keys are not written. static_scratch: call
         colibri_moe_forward_static (working memory in the library's fixed
         per-GPU array instead of the handle's)."""
+        return self._call(colibri_moe_forward_static if static_scratch else colibri_moe_forward, x, y, routing)
+
+    def forward_few(self, x, y=None, routing: dict | None = None):
+        """forward for at most FEW_TOKENS tokens in two kernels
+        (colibri_moe_forward_few; bf16 layers)."""
+        return self._call(colibri_moe_forward_few, x, y, routing)
+
+    def _call(self, fn, x, y, routing):
         torch = self._torch
         if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != self.d or not x.is_contiguous():
             raise TypeError("x must be a contiguous [T][d] tensor of the layer dtype")
@@ -310,7 +327,6 @@ class MoELayer:
         if routing is not None:
             r = Routing(*[routing[n].data_ptr() if routing.get(n) is not None else None
                           for n, _ in Routing._fields_])
-        fn = colibri_moe_forward_static if static_scratch else colibri_moe_forward
         st = fn(self.handle, x.data_ptr(), T, y.data_ptr(), r)
         if st != OK:
             raise ColibriError(fn.__name__, st)

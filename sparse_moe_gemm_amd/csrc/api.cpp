@@ -26,6 +26,7 @@ constexpr uint32_t kMagic = 0xC011B41Eu;
 constexpr int kStages = 6;
 constexpr int32_t kMaxTokensLimit = 1 << 24;
 constexpr size_t kMxBlockValues = 32;  // values per scale byte of the 4-bit format
+static_assert(COLIBRI_MOE_FEW_TOKENS == kFewTokens, "header and kernels agree");
 
 const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_up_gemm",
                                           "gate_up_reduce", "down_gemm", "combine"};
@@ -74,6 +75,7 @@ struct colibri_moe {
     bool mx4;     // 4-bit microscaled expert weights
     bool q4;      // and token rows for the gate/up GEMM
     Workspace ws; // in the arena, sized for max_tokens
+    uint16_t* few_h;  // h of colibri_moe_forward_few [2][few tokens * k][f], bf16 layers
     int32_t* ccnt;  // fused combine: arrivals per token and 128-column tile [max_tokens][d/128], zero between calls
     bool timing;
     hipEvent_t ev[kStages + 1];
@@ -288,6 +290,8 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     const size_t o_sgu = h->fp8 ? cv.take(E * 2 * f * sizeof(float)) : 0;
     const size_t o_sd = h->fp8 ? cv.take(E * d * sizeof(float)) : 0;
     const size_t o_ccnt = h->fuse_combine ? cv.take((size_t)c.max_tokens * (d / 128) * sizeof(int32_t)) : 0;
+    const size_t few_rows = (size_t)std::min(c.max_tokens, (int32_t)COLIBRI_MOE_FEW_TOKENS) * c.top_k;
+    const size_t o_few = c.dtype == COLIBRI_MOE_BF16 ? cv.take(2 * few_rows * f * sizeof(uint16_t)) : 0;
     const size_t o_ws = cv.take(layout_workspace(h, c.max_tokens, true, nullptr, nullptr));
     h->arena_bytes = cv.off;
 
@@ -306,6 +310,7 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     h->m_gu = h->mx4 ? base + o_mgu : nullptr;
     h->m_d = h->mx4 ? base + o_md : nullptr;
     h->ccnt = h->fuse_combine ? (int32_t*)(base + o_ccnt) : nullptr;
+    h->few_h = c.dtype == COLIBRI_MOE_BF16 ? (uint16_t*)(base + o_few) : nullptr;
     layout_workspace(h, c.max_tokens, true, base + o_ws, &h->ws);
 
     hipStream_t s = h->stream;
@@ -675,6 +680,75 @@ colibri_moe_status_t colibri_moe_forward_static(colibri_moe_t* h, const void* x,
     return forward_impl(h, x, T, y, ro, ws, false);
 }
 
+colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, int32_t T, void* y,
+                                             const colibri_moe_routing_t* r)
+{
+    colibri_moe_routing_t ro;
+    bool skip;
+    const colibri_moe_status_t st = check_call(h, x, T, y, r, &ro, &skip);
+    if (st != COLIBRI_MOE_OK)
+        return st;
+    const colibri_moe_config_t& c = h->cfg;
+    // 2^20: offsets into h are 32-bit byte offsets
+    if (c.dtype != COLIBRI_MOE_BF16 || c.d_ff > 1 << 20)
+        return COLIBRI_MOE_ERR_UNSUPPORTED;
+    if (T > COLIBRI_MOE_FEW_TOKENS)
+        return COLIBRI_MOE_ERR_TOO_LARGE;
+    if (skip)
+        return COLIBRI_MOE_OK;
+    hipStream_t s = h->stream;
+    const bool tm = h->timing;
+    FewArgs a{};
+    a.x = x;
+    a.w_rt = h->w_rt;
+    a.b = h->b_r;
+    a.w_gu = h->w_gu;
+    a.w_d = h->w_d;
+    a.s_gu = h->s_gu;
+    a.s_d = h->s_d;
+    a.m_gu = h->m_gu;
+    a.m_d = h->m_d;
+    a.act_quant = h->q8 || h->q4;
+    a.routed = !few_routes_itself(c.d_model, c.n_experts);
+    a.T = T;
+    a.d = c.d_model;
+    a.E = c.n_experts;
+    a.k = c.top_k;
+    a.f = c.d_ff;
+    a.logits = ro.logits;
+    a.ids = ro.topk_ids ? ro.topk_ids : h->ws.ids;
+    a.w = ro.topk_w ? ro.topk_w : h->ws.topw;
+    a.counts = ro.expert_counts;
+    a.offsets = ro.expert_offsets;
+    a.perm = ro.perm;
+    a.perm_slot = ro.perm_slot;
+    a.inv = ro.inv;
+    a.h = h->few_h;
+    a.y = y;
+    if (tm)
+        CMOE_HIP(hipEventRecord(h->ev[0], s));
+    if (a.routed) {
+        RouterArgs ra{x, h->w_rt, h->b_r, T, c.d_model, c.n_experts, c.top_k, ro.logits, a.ids, a.w};
+        CMOE_HIP(launch_router_bf16(ra, s));
+    }
+    if (tm) {
+        CMOE_HIP(hipEventRecord(h->ev[1], s));
+        CMOE_HIP(hipEventRecord(h->ev[2], s));
+    }
+    CMOE_HIP(launch_few_gate_up(a, h->cus, s));
+    if (tm) {
+        CMOE_HIP(hipEventRecord(h->ev[3], s));
+        CMOE_HIP(hipEventRecord(h->ev[4], s));
+    }
+    CMOE_HIP(launch_few_down(a, h->cus, s));
+    if (tm) {
+        CMOE_HIP(hipEventRecord(h->ev[5], s));
+        CMOE_HIP(hipEventRecord(h->ev[6], s));
+    }
+    if (!(c.flags & COLIBRI_MOE_FLAG_ASYNC))
+        CMOE_HIP(hipStreamSynchronize(s));
+    return COLIBRI_MOE_OK;
+}
 
 colibri_moe_status_t colibri_moe_free(colibri_moe_t* h)
 {
@@ -766,7 +840,7 @@ const char* colibri_moe_status_string(colibri_moe_status_t s)
     case COLIBRI_MOE_ERR_HIP:
         return "HIP runtime error";
     case COLIBRI_MOE_ERR_TOO_LARGE:
-        return "batch needs more working memory than the static scratch array holds";
+        return "batch too large for this entry point (static scratch array, or few-token limit)";
     }
     return "unknown status";
 }

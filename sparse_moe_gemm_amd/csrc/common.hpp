@@ -264,6 +264,39 @@ struct MxDecodeArgs {
 int decode_mx_split(int E, int N, int K, int waves);
 hipError_t launch_decode_mx(const MxDecodeArgs& a, int gate_up, int cus, hipStream_t s);
 
+// The whole layer for at most kFewTokens tokens in two launches (few.hip),
+// bf16 layers of any weight precision.
+constexpr int kFewTokens = 16;
+struct FewArgs {
+    const void* x;         // [T][d] bf16
+    const void* w_rt;      // router weights (router_weight_bytes layout), bias [E]
+    const float* b;
+    const void* w_gu;      // expert weights as the other GEMMs read them, with
+    const void* w_d;       //   fp8 row scales (s_gu, s_d) or 4-bit scale bytes
+    const float* s_gu;     //   (m_gu, m_d), else null
+    const float* s_d;
+    const uint8_t* m_gu;
+    const uint8_t* m_d;
+    int act_quant;         // the layer quantizes its token rows for gate/up
+    int routed;            // ids and w already hold the routing
+    int T, d, E, k, f;
+    float* logits;         // routing outputs; ids and w are required, the others may be null
+    int32_t* ids;
+    float* w;
+    int32_t* counts;
+    int32_t* offsets;
+    int32_t* perm;
+    int32_t* perm_slot;
+    int32_t* inv;
+    uint16_t* h;           // [2][T*k][f] bf16: high and low parts
+    void* y;               // [T][d] bf16
+};
+// Whether the first launch computes the routing (else launch_router_bf16 runs
+// before it).
+bool few_routes_itself(int d, int E);
+hipError_t launch_few_gate_up(const FewArgs& a, int cus, hipStream_t s);
+hipError_t launch_few_down(const FewArgs& a, int cus, hipStream_t s);
+
 struct CombineArgs {
     const float* ys;    // split partials, each [A][d] fp32 by sorted position (ys_bf16: one [A][d] bf16)
     const int32_t* inv; // [A]: sorted position of assignment t*k+j

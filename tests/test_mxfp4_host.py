@@ -93,6 +93,20 @@ def test_init_rejects_bad_4_bit_configs(kw, status):
     assert st == status and not h
 
 
+def test_forward_few_rejects_unknown_handles():
+    assert cm.colibri_moe_forward_few(None, FAKE, 4, FAKE) == cm.ERR_INVALID_ARG
+    assert cm.colibri_moe_forward_few(FAKE, FAKE, 4, FAKE) == cm.ERR_INVALID_ARG
+
+
+def test_few_token_limit_matches_the_header():
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "colibri_moe.h")).read()
+    assert int(re.search(r"#define COLIBRI_MOE_FEW_TOKENS (\d+)", text).group(1)) == cm.FEW_TOKENS
+
+
 def test_python_wrappers_reject_wrong_tensors():
     import torch
 
