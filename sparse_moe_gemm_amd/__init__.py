@@ -164,38 +164,46 @@ def quantize_fp8(w, stream=None):
 
 def colibri_moe_quantize_mxfp4(w_ptr: int, dtype: int, rows: int, cols: int, row_stride: int, codes_ptr: int,
                                scales_ptr: int, hip_stream: int = 0) -> int:
-    return lib().colibri_moe_quantize_mxfp4(ctypes.c_void_p(w_ptr), dtype, rows, cols, row_stride,
-                                            ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr),
-                                            ctypes.c_void_p(hip_stream))
+    return lib().colibri_moe_quantize_mxfp4(w_ptr, dtype, rows, cols, row_stride, codes_ptr, scales_ptr, hip_stream)
 
 
 def colibri_moe_dequantize_mxfp4(codes_ptr: int, scales_ptr: int, rows: int, cols: int, dtype: int, out_ptr: int,
                                  hip_stream: int = 0) -> int:
-    return lib().colibri_moe_dequantize_mxfp4(ctypes.c_void_p(codes_ptr), ctypes.c_void_p(scales_ptr), rows, cols,
-                                              dtype, ctypes.c_void_p(out_ptr), ctypes.c_void_p(hip_stream))
+    return lib().colibri_moe_dequantize_mxfp4(codes_ptr, scales_ptr, rows, cols, dtype, out_ptr, hip_stream)
+
+
+def _on_device_of(t, fn):
+    """fn() with t's device current (the kernels run on the current one)."""
+    import torch
+
+    if t.device.index == torch.cuda.current_device():
+        return fn()
+    with torch.cuda.device(t.device):
+        return fn()
 
 
 def quantize_mxfp4(w, stream=None):
     """(codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]) of a 2-D
     bf16 or fp32 device tensor whose rows are contiguous (they may be slices of
     longer ones): the 4-bit microscaled codes a layer built with
-    FLAG_MXFP4_WEIGHTS keeps. cols must be a multiple of 32."""
+    FLAG_MXFP4_WEIGHTS keeps. cols must be a multiple of 32. The work is
+    enqueued on `stream`, by default the current one."""
     import torch
 
-    if w.dtype not in (torch.bfloat16, torch.float32) or w.dim() != 2 or not w.is_cuda:
+    bf16 = w.dtype == torch.bfloat16
+    if not (bf16 or w.dtype == torch.float32) or w.dim() != 2 or not w.is_cuda:
         raise TypeError("w must be a 2-D bfloat16 or float32 device tensor")
     rows, cols = w.shape
-    if cols % 32 != 0 or (cols > 1 and w.stride(1) != 1) or (rows > 1 and w.stride(0) < cols):
+    row_stride, step = w.stride()
+    if cols % 32 != 0 or (cols > 1 and step != 1) or (rows > 1 and row_stride < cols):
         raise ValueError("rows must be contiguous, a multiple of 32 long, and must not overlap")
-    with torch.cuda.device(w.device):
-        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
-        scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device=w.device)
-        if w.numel() == 0:
-            return codes, scales
-        s = stream if stream is not None else torch.cuda.current_stream()
-        st = colibri_moe_quantize_mxfp4(w.data_ptr(), BF16 if w.dtype == torch.bfloat16 else F32, rows, cols,
-                                        w.stride(0) if rows > 1 else cols, codes.data_ptr(), scales.data_ptr(),
-                                        s.cuda_stream)
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=w.device)
+    if rows == 0 or cols == 0:
+        return codes, scales
+    st = _on_device_of(w, lambda: colibri_moe_quantize_mxfp4(
+        w.data_ptr(), BF16 if bf16 else F32, rows, cols, row_stride if rows > 1 else cols, codes.data_ptr(),
+        scales.data_ptr(), (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
     if st != OK:
         raise ColibriError("colibri_moe_quantize_mxfp4", st)
     return codes, scales
@@ -204,11 +212,12 @@ def quantize_mxfp4(w, stream=None):
 def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     """The values [rows][cols] (bf16 by default, or fp32) of 4-bit microscaled
     rows: contiguous uint8 device tensors codes [rows][cols/2] and scales
-    [rows][cols/32]. Exact."""
+    [rows][cols/32]. Exact. The work is enqueued on `stream`, by default the
+    current one."""
     import torch
 
-    dtype = torch.bfloat16 if dtype is None else dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    bf16 = dtype is None or dtype == torch.bfloat16
+    if not (bf16 or dtype == torch.float32):
         raise TypeError("dtype must be bfloat16 or float32")
     for t in (codes, scales):
         if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
@@ -216,13 +225,12 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     rows, cols = codes.shape[0], codes.shape[1] * 2
     if scales.device != codes.device or scales.shape[0] != rows or scales.shape[1] * 32 != cols:
         raise ValueError("codes [rows][cols/2] and scales [rows][cols/32] do not belong together")
-    with torch.cuda.device(codes.device):
-        out = torch.empty(rows, cols, dtype=dtype, device=codes.device)
-        if out.numel() == 0:
-            return out
-        s = stream if stream is not None else torch.cuda.current_stream()
-        st = colibri_moe_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                          BF16 if dtype == torch.bfloat16 else F32, out.data_ptr(), s.cuda_stream)
+    out = torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32, device=codes.device)
+    if rows == 0 or cols == 0:
+        return out
+    st = _on_device_of(codes, lambda: colibri_moe_dequantize_mxfp4(
+        codes.data_ptr(), scales.data_ptr(), rows, cols, BF16 if bf16 else F32, out.data_ptr(),
+        (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
     if st != OK:
         raise ColibriError("colibri_moe_dequantize_mxfp4", st)
     return out

@@ -248,6 +248,15 @@ size_t layout_workspace(const colibri_moe* h, int64_t T, bool up_to, uint8_t* ba
     // Ys: the down GEMM's partial sums (kMaxSplit for bf16), and on the
     // small-batch path also the gate/up slice partials before SiLU.
     size_t ys_floats = (c.dtype == COLIBRI_MOE_BF16 ? (size_t)cmoe::kMaxSplit : 1) * A * d;
+    if (h->mx4) {
+        // partial rows of the largest call: calls past mx_split_rows() rows do
+        // not split, the smaller ones are looked at one by one
+        size_t rows = A;
+        const int64_t most = std::min<int64_t>(T, mx_split_rows(h->cus) / (int64_t)k + 1);
+        for (int64_t t = up_to ? 1 : T; t <= (up_to ? most : T); ++t)
+            rows = std::max(rows, (size_t)t * k * mx_down_split((int)(t * k), (int)E, (int)d, (int)f, h->cus));
+        ys_floats = rows * d;
+    }
     // (calls with A <= dec_max_a may take the small-batch path)
     if (c.dtype == COLIBRI_MOE_BF16 && h->dec_max_a > 0 && (up_to || A <= (size_t)h->dec_max_a)) {
         const size_t ad = std::min(A, (size_t)h->dec_max_a);
@@ -431,23 +440,21 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     h->dec_max_a = 0;
     h->dec_gate_rows = 0;
     h->dec_split_gu = h->dec_split_dn = 1;
-    if (cfg->dtype == COLIBRI_MOE_BF16) {
+    if (cfg->dtype == COLIBRI_MOE_BF16 && !h->mx4) {
         const int64_t amax = (int64_t)cfg->max_tokens * cfg->top_k;
         h->dec_max_a = (int)std::min<int64_t>(amax, env_int("CMOE_DECODE_MAX_A", 2048, 0, 1 << 16));
-        h->dec_gate_rows = env_int("CMOE_DECODE_MAX_ROWS", h->fp8 || h->mx4 ? 32 : 48, 0, 1 << 16);
+        h->dec_gate_rows = env_int("CMOE_DECODE_MAX_ROWS", h->fp8 ? 32 : 48, 0, 1 << 16);
         const int waves = cmoe::decode_waves(h->cus);
         // k step of the small-batch kernels: 16 (bf16 weights), 32 (8-bit
         // weights), 64 (8-bit token rows, gate/up only)
         const int kstep_dn = h->fp8 ? 32 : 16;
         const int kstep_gu = h->q8 ? 64 : kstep_dn;
-        h->dec_split_gu = h->mx4 ? cmoe::decode_mx_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, waves)
-                                 : cmoe::decode_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, kstep_gu, waves, 64);
+        h->dec_split_gu = cmoe::decode_split(cfg->n_experts, 2 * cfg->d_ff, cfg->d_model, kstep_gu, waves, 64);
         // No K slices: the gate/up items write H themselves (SiLU(g)*u in
         // their epilogue) instead of partials for a separate sum pass
         // (CMOE_DECODE_FUSE_SILU=0 keeps the pass)
         h->dec_fuse_silu = h->dec_split_gu == 1 && env_int("CMOE_DECODE_FUSE_SILU", 1, 0, 1) != 0;
-        h->dec_split_dn = h->mx4 ? cmoe::decode_mx_split(cfg->n_experts, cfg->d_model, cfg->d_ff, waves)
-                                 : cmoe::decode_split(cfg->n_experts, cfg->d_model, cfg->d_ff, kstep_dn, waves, 64);
+        h->dec_split_dn = cmoe::decode_split(cfg->n_experts, cfg->d_model, cfg->d_ff, kstep_dn, waves, 64);
     }
     st = init_impl(h, w);
     if (st != COLIBRI_MOE_OK) {
@@ -515,13 +522,7 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     const int gate = small && h->dec_gate_rows > 0 && T > h->dec_gate_rows ? h->dec_gate_rows : 0;
     const bool tiled = !small || gate > 0;
     const bool order_m = (int64_t)A <= (int64_t)h->order_m_rows * c.n_experts;
-    const bool mx_small_tiles = (int64_t)A <= (int64_t)128 * c.n_experts;
-    if (small && mx4) {
-        MxDecodeArgs gu{q4 ? (const void*)ws.xq : x, q4 ? ws.xsb : nullptr, h->w_gu, h->m_gu, ws.Ys, offsets, perm,
-                        A, c.n_experts, c.d_model, c.d_ff, h->dec_split_gu,
-                        h->dec_fuse_silu ? (uint16_t*)ws.H : nullptr, gate};
-        CMOE_HIP(launch_decode_mx(gu, 1, h->cus, s));
-    } else if (small) {
+    if (small) {
         DecodeArgs gu{q8 ? (const void*)ws.xq : x, h->w_gu, h->s_gu, q8 ? ws.xsc : nullptr, ws.Ys, offsets, perm,
                       A, c.n_experts, c.d_model, c.d_ff, h->dec_split_gu};
         gu.h = h->dec_fuse_silu ? (uint16_t*)ws.H : nullptr;
@@ -529,10 +530,9 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
         gu.gate_rows = gate;
         CMOE_HIP(launch_decode_gemm(gu, 1, h->cus, s));
     }
-    if (tiled && mx4) {
+    if (mx4) {
         MxGemmArgs gu{q4 ? (const void*)ws.xq : x, q4 ? ws.xsb : nullptr, h->w_gu, h->m_gu, ws.H, offsets, perm,
-                      A, c.n_experts, c.top_k, c.d_model, c.d_ff, order_m ? -8 : h->group_n_gu, 1, h->cus,
-                      mx_small_tiles ? 1 : 0, gate};
+                      A, c.n_experts, c.top_k, c.d_model, c.d_ff, order_m ? -8 : h->group_n_gu, 1, h->cus};
         CMOE_HIP(launch_gate_up_mx(gu, s));
     } else if (tiled) {
         GemmArgs gu{q8 ? (const void*)ws.xq : x, h->w_gu, h->s_gu, q8 ? ws.xsc : nullptr, ws.H, offsets, perm, A,
@@ -558,12 +558,7 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     int split = 1;
     bool fused = false;    // combine done by the down GEMM
     int ys_bf16 = 0;       // expert outputs stored as bf16
-    if (small && mx4) {
-        MxDecodeArgs dn{ws.H, nullptr, h->w_d, h->m_d, ws.Ys, offsets, perm, A, c.n_experts, c.d_model, c.d_ff,
-                        h->dec_split_dn, nullptr, gate};
-        CMOE_HIP(launch_decode_mx(dn, 0, h->cus, s));
-        split = h->dec_split_dn;
-    } else if (small) {
+    if (small) {
         DecodeArgs dn{ws.H, h->w_d, h->s_d, nullptr, ws.Ys, offsets, perm,
                       A, c.n_experts, c.d_model, c.d_ff, h->dec_split_dn};
         dn.max_rows = T;
@@ -571,10 +566,10 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
         CMOE_HIP(launch_decode_gemm(dn, 0, h->cus, s));
         split = h->dec_split_dn;
     }
-    if (tiled && mx4) {
-        split = down_split_bf16(A, c.n_experts, c.d_model, c.d_ff, h->cus, 1);
+    if (mx4) {
+        split = mx_down_split(A, c.n_experts, c.d_model, c.d_ff, h->cus);
         MxGemmArgs dn{ws.H, nullptr, h->w_d, h->m_d, ws.Ys, offsets, perm, A, c.n_experts, c.top_k, c.d_model, c.d_ff,
-                      order_m ? -8 : h->group_n_dn, split, h->cus, mx_small_tiles ? 1 : 0, gate};
+                      order_m ? -8 : h->group_n_dn, split, h->cus};
         CMOE_HIP(launch_down_mx(dn, s));
     } else if (tiled) {
         split = bf ? down_split_bf16(A, c.n_experts, c.d_model, c.d_ff, h->cus, 0) : 1;

@@ -241,28 +241,13 @@ struct MxGemmArgs {
     int group_n;              // tile order (tiles.hpp)
     int split;                // K splits of the down GEMM
     int cus;
-    int small_tiles;          // 1: tiles of 64 rows, 0: of 256
-    int skip_rows;            // as GemmArgs
 };
+// K splits the down GEMM uses for a call with A = T*k assignments.
+constexpr int kMxMaxSplit = 4;
+int mx_down_split(int A, int E, int d, int f, int cus);
+int64_t mx_split_rows(int cus);  // calls of more assignments are not split
 hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s);
 hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s);
-
-// Small-batch GEMMs on 4-bit weights (decode_mxfp4.hip); fields as DecodeArgs.
-struct MxDecodeArgs {
-    const void* a;
-    const uint8_t* a_scales;  // gate/up on 4-bit token rows; else null
-    const void* b;
-    const uint8_t* b_scales;
-    float* part;
-    const int32_t* offsets;
-    const int32_t* perm;
-    int A, E, d, f;
-    int split;
-    uint16_t* h;
-    int gate_rows;
-};
-int decode_mx_split(int E, int N, int K, int waves);
-hipError_t launch_decode_mx(const MxDecodeArgs& a, int gate_up, int cus, hipStream_t s);
 
 // The whole layer for at most kFewTokens tokens in two launches (few.hip),
 // bf16 layers of any weight precision.

@@ -52,7 +52,7 @@ struct Unit {
     static constexpr int K = 32 * M;
     static constexpr int kCG = FMT == kMx4 ? 2 : 1;  // gate/up: 16-column groups per item
     static constexpr int kXU = kXV / M;              // units of token fragments kept
-    static constexpr int kUPS = FMT == kMx4 ? 2 : 4; // units per step (eight loads)
+    static constexpr int kUPS = FMT == kMx4 ? 1 : 4; // units per step
 };
 
 // Byte offset of lane l's 16 bytes for rows 16 cj .. +16 of a 32-row block from
@@ -64,12 +64,12 @@ __device__ __forceinline__ uint32_t unit_lane(int cj, int lane)
     return (uint32_t)((o >> 1) * kWave + (o & 1) * 32 + 16 * cj + (lane & 15)) * 16u;
 }
 
-// MXFP4: the scale byte of that lane's 32 codes, from the first byte of the
-// unit's scale group (its two blocks are bytes 2 (u%2) + 0, 1 of the words).
+// MXFP4: the scale byte of that lane's 32 codes, from the row block's part of
+// the unit's scales (its two blocks kb are lane halves o/2 here).
 __device__ __forceinline__ uint32_t unit_scale_lane(int cj, int lane)
 {
     const int o = lane >> 4;
-    return (uint32_t)((o & 1) * 32 + 16 * cj + (lane & 15)) * 4u + (uint32_t)(o >> 1);
+    return (uint32_t)((o & 1) * 32 + 16 * cj + (lane & 15)) * 2u + (uint32_t)(o >> 1);
 }
 
 // A wave-uniform address in scalar registers, so that the loads from it take a
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
     const int items = nact * groups;
     const int mine = (int)blockIdx.x < items ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     const int Q = mine * P;
-    const int KB = 2 * NU, KG = mx_scale_groups(g.d), NBK = g.f / 16;  // 32-row blocks of [2f]
+    const int KB = 2 * NU, NBK = g.f / 16;  // 32-row blocks of [2f]
 
     const uint32_t lane_w = unit_lane(0, lane), lane_m = unit_scale_lane(0, lane);
 
@@ -436,10 +436,11 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
                 for (int h = 0; h < CG; ++h)
                     t.w[i][n][h] = __builtin_nontemporal_load((const Vec16*)(wp + lane_w + h * 256));
                 if constexpr (FMT == kMx4) {
-                    const uint8_t* mp = uniform(g.m_gu + (rb * KG + u / 2) * 256 + 2 * (u & 1));
+                    const int nb = 2 * c + n;
+                    const uint8_t* mp = uniform(g.m_gu + mx_scale_group(e, nb, u, 2 * g.f, g.d) + mx_scale_at(nb, 0, 0));
 #pragma unroll
                     for (int h = 0; h < CG; ++h)
-                        t.mx[i][n][h] = mp[lane_m + h * 64];
+                        t.mx[i][n][h] = mp[lane_m + h * 32];
                 }
             }
             if constexpr (FMT == kFp8)
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
 {
     using U = Unit<FMT>;
     constexpr int M = U::M;
-    constexpr int B = FMT == kBf16 ? 4 : FMT == kFp8 ? 2 : 1;
+    constexpr int B = FMT == kBf16 ? 3 : FMT == kFp8 ? 2 : 1;
     __shared__ Routes r;
     __shared__ float red[kWaves][256];
 
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
     const int nact = build_routes(r, g.T, g.k);
     const int NU = g.f / U::K;   // units per expert
     const int V = nact * NU;     // of the item, over its experts
-    const int KB = 2 * NU, KG = mx_scale_groups(g.f), NBK = g.d / 32;
+    const int KB = 2 * NU, NBK = g.d / 32;
     const uint32_t plane = (uint32_t)A * (uint32_t)g.f * 2u;
     const __amdgpu_buffer_rsrc_t rh = __builtin_amdgcn_make_buffer_rsrc((void*)g.h, 0, (int)(2 * plane), 0x00020000);
 
@@ -575,7 +576,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
                 t.w[b] = __builtin_nontemporal_load(
                     (const Vec16*)(uniform((const uint8_t*)g.w_d + (rb * KB + 2 * u) * 1024) + lane_w));
                 if constexpr (FMT == kMx4)
-                    t.mx[b] = uniform(g.m_d + (rb * KG + u / 2) * 256 + 2 * (u & 1))[lane_m];
+                    t.mx[b] = uniform(g.m_d + mx_scale_group(e, n / 2, u, g.d, g.f) + mx_scale_at(n / 2, 0, 0))[lane_m];
                 if constexpr (FMT == kFp8)
                     t.sc[b] = g.s_d[rb * 32 + 16 * (n & 1) + (lane & 15)];
                 // past the buffer for lanes that hold zeros

@@ -16,11 +16,11 @@
 //
 // A tile is BM sorted rows of one expert x 256 weight rows (x a K split); a
 // persistent workgroup walks its tiles (tiles.hpp) and streams their K stages
-// (64 k of bf16 rows, 128 k of 4-bit rows) through a ring of three LDS slots:
-// while stage s is multiplied, stage s + 1 has landed or is landing and stage
-// s + 2 is requested, across tile borders too. One wait and one barrier per
-// stage: after it every wave's loads of stage s are in LDS and every wave has
-// read stage s - 1 to the end, so its slot can take stage s + 2.
+// (64 k of bf16 rows, 128 k of 4-bit rows) through a ring of SLOTS LDS slots:
+// while stage s is multiplied, the next SLOTS - 1 are on their way, across tile
+// borders too. One wait and one barrier per stage: after it every wave's loads
+// of stage s are in LDS and every wave has read stage s - 1 to the end, so its
+// slot can take stage s + SLOTS - 1.
 // Waves form WAVES_M x 4; a wave multiplies WM = BM / WAVES_M rows with 64
 // weight rows (one gate and one up block of 32, so SiLU(g)*u stays in its
 // registers). The weight fragment is the MFMA's first operand: a result lane
@@ -35,8 +35,7 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-constexpr int kBN = 256;   // weight rows per tile
-constexpr int kSlots = 3;  // LDS stages
+constexpr int kBN = 256;  // weight rows per tile
 
 __device__ __forceinline__ float silu_fast(float z)
 {
@@ -50,15 +49,15 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b)
 
 // One K stage: BM token rows of RB bytes (64 k as bf16, 128 k as codes), their
 // scale words (A4: bytes of the row's four blocks), KBS 1 KiB weight blocks
-// for each 32 weight rows and the scale group they belong to.
+// for each 32 weight rows and the scales of the 128 k they belong to.
 template <int BM, bool A4>
 struct MxStage {
     static constexpr int RB = A4 ? 64 : 128;
     static constexpr int KBS = A4 ? 2 : 1;
     Vec16 a[BM * RB / 16];
     Vec16 b[(kBN / 32) * KBS * kWave];
-    uint32_t bs[(kBN / 32) * kWave];
-    uint32_t as[A4 ? BM : 1];
+    uint16_t bs[(kBN / 32) * kWave];
+    uint32_t as[A4 ? (BM < kWave ? kWave : BM) : 4];
 };
 
 // Position of 16-byte chunk c of tile row r in the stage: the 16 rows that 16
@@ -74,12 +73,15 @@ struct MxShape {
     using Stage = MxStage<BM, A4>;
     static constexpr int NW = WAVES_M * 4;
     static constexpr int WM = BM / WAVES_M;
-    static constexpr int ROWS = A4 ? 16 : 8;            // tile rows per 1 KiB load
-    static constexpr int A_INS = BM / ROWS / NW;        // loads per wave and stage
+    static constexpr int ROWS = A4 ? 16 : 8;  // tile rows per 1 KiB load
+    // Loads per wave and stage. Every wave issues as many (the waits count
+    // them); where there are fewer loads than waves, waves share one and write
+    // the same data to the same place.
+    static constexpr int A_ALL = BM / ROWS, A_INS = A_ALL < NW ? 1 : A_ALL / NW;
     static constexpr int B_INS = (kBN / 32) * Stage::KBS / NW;
-    static constexpr int S_INS = (kBN / 32) / NW;
-    static constexpr int NLD = A_INS + B_INS + S_INS + (A4 ? 1 : 0);
-    static_assert(A_INS >= 1 && B_INS >= 1 && S_INS >= 1, "every wave loads a share");
+    static constexpr int AS_ALL = BM < kWave ? 1 : BM / kWave;
+    static constexpr int NLD = A_INS + B_INS + 1 + (A4 ? 1 : 0);
+    static_assert(B_INS >= 1, "every wave loads a share");
 };
 
 // Where the next stage to load comes from: a position in the stream of all K
@@ -93,7 +95,7 @@ struct MxCursor {
     int L;                 // the tile's launch index
 };
 
-template <int BM, int WAVES_M, bool A4, bool GATE_UP>
+template <int BM, int WAVES_M, int SLOTS, bool A4, bool GATE_UP>
 __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx_gemm_kernel(
     MxGemmArgs g)
 {
@@ -101,12 +103,12 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
     using Stage = typename Sh::Stage;
     constexpr int SM = GATE_UP ? 0 : 64;  // tile order as in the other GEMMs
     constexpr int MI = Sh::WM / 32;
-    __shared__ Stage ring[kSlots];
+    __shared__ Stage ring[SLOTS];
 
     const int N = GATE_UP ? 2 * g.f : g.d;
     const int K = GATE_UP ? g.d : g.f;
     const int NT = (N + kBN - 1) / kBN;
-    const int KB = K / 64, KG = mx_scale_groups(K);
+    const int KB = K / 64;
     const int KT = K / (A4 ? 128 : 64);
     const int S = GATE_UP ? 1 : g.split;
     const int lane = threadIdx.x % kWave;
@@ -116,8 +118,6 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 
     TileTable tt;
     const int total = make_table<BM, SM>(g.offsets, g.E, lane, NT * S, tt);
-    if (g.skip_rows > 0 && table_max_rows(tt) <= g.skip_rows)
-        return;  // the small-batch kernels take this call
     const int GRID = gridDim.x;
     if ((int)blockIdx.x >= total)
         return;
@@ -138,15 +138,15 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
         const int nb0 = t.n * (kBN / 32), nbs = N / 32 - nb0;  // row blocks from here to the expert's end
         const int64_t blk = (int64_t)t.e * (N / 32) + nb0;
         c.rb = buffer_rsrc((const uint8_t*)g.b + blk * KB * 1024, (uint32_t)min(nbs, kBN / 32) * (uint32_t)KB * 1024u);
-        c.rs = buffer_rsrc(g.b_scales + blk * KG * 256, (uint32_t)min(nbs, kBN / 32) * (uint32_t)KG * 256u);
+        c.rs = buffer_rsrc(g.b_scales + mx_scale_group(t.e, nb0, 0, N, K), (uint32_t)(K / 128) * 1024u);
 #pragma unroll
         for (int q = 0; q < Sh::A_INS; ++q) {
             const int per = Sh::Stage::RB / 16;  // chunks per row
-            const int r = (wv * Sh::A_INS + q) * Sh::ROWS + lane / per;
+            const int r = (wv * Sh::A_INS + q) % Sh::A_ALL * Sh::ROWS + lane / per;
             c.aoff[q] = row_of(t, r) * Kbytes + (uint32_t)mx_swz<A4>(r, lane % per) * 16u;
         }
         if constexpr (A4)
-            c.asoff = row_of(t, (wv % (BM / 64)) * 64 + lane) * (uint32_t)(K / 32);
+            c.asoff = row_of(t, (wv % Sh::AS_ALL) * kWave + lane) * (uint32_t)(K / 32);
         c.kt = t.kt0;
         c.left = t.nkt;
         c.L = L;
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
         for (int q = 0; q < Sh::A_INS; ++q)
             lds_load16(ra, c.aoff[q], (uint32_t)c.kt * (uint32_t)Stage::RB,
-                       base + (uint32_t)offsetof(Stage, a) + (uint32_t)(wv * Sh::A_INS + q) * 1024u);
+                       base + (uint32_t)offsetof(Stage, a) + (uint32_t)((wv * Sh::A_INS + q) % Sh::A_ALL) * 1024u);
 #pragma unroll
         for (int q = 0; q < Sh::B_INS; ++q) {
             const int i = wv * Sh::B_INS + q;  // row block i / KBS, k block i % KBS of the stage
@@ -167,15 +167,11 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
                        ((uint32_t)(i / Stage::KBS) * (uint32_t)KB + (uint32_t)(c.kt * Stage::KBS + i % Stage::KBS)) * 1024u,
                        base + (uint32_t)offsetof(Stage, b) + (uint32_t)i * 1024u);
         }
-#pragma unroll
-        for (int q = 0; q < Sh::S_INS; ++q) {
-            const int i = wv * Sh::S_INS + q;
-            lds_load4(c.rs, lane4, ((uint32_t)i * (uint32_t)KG + (uint32_t)(c.kt * Stage::KBS / 4)) * 256u,
-                      base + (uint32_t)offsetof(Stage, bs) + (uint32_t)i * 256u);
-        }
+        lds_load4(c.rs, lane4, (uint32_t)(c.kt * Stage::KBS / 2) * 1024u + (uint32_t)(wv % 4) * 256u,
+                  base + (uint32_t)offsetof(Stage, bs) + (uint32_t)(wv % 4) * 256u);
         if constexpr (A4)
             lds_load4(ras, c.asoff, (uint32_t)c.kt * 4u,
-                      base + (uint32_t)offsetof(Stage, as) + (uint32_t)(wv % (BM / 64)) * 256u);
+                      base + (uint32_t)offsetof(Stage, as) + (uint32_t)(wv % Sh::AS_ALL) * 256u);
         if (c.left > 1) {
             ++c.kt;
             --c.left;
@@ -186,8 +182,9 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 
     MxCursor<Sh::A_INS> cur;
     open(cur, blockIdx.x);
-    request(cur, 0);
-    request(cur, 1);
+#pragma unroll
+    for (int q = 0; q < SLOTS - 1; ++q)
+        request(cur, q);
     int slot = 0;
 
     for (int L = blockIdx.x; L < total; L += GRID) {
@@ -209,11 +206,11 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
             for (int j = 0; j < t.nkt; ++j) {
                 // (LDS reads too: the compiler may move the MFMAs that use them
                 // past the barrier, and their waits with them)
-                wait_vm<Sh::NLD>();
+                wait_vm<Sh::NLD * (SLOTS - 2)>();
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                request(cur, slot == 0 ? 2 : slot - 1);
+                request(cur, slot == 0 ? SLOTS - 1 : slot - 1);
                 const Stage& st = ring[slot];
                 const int kb = (t.kt0 + j) * Stage::KBS;
                 if constexpr (RGC > 0) {
@@ -221,7 +218,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
                         uint32_t sb[2], sa[RGC];
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
-                            sb[n] = st.bs[(wn * 2 + n) * kWave + lane] >> (8 * (kb & 3));
+                            sb[n] = st.bs[(wn * 2 + n) * kWave + lane];
 #pragma unroll
                         for (int i = 0; i < RGC; ++i)
                             sa[i] = st.as[wm * Sh::WM + i * 32 + (lane & 31)] >> (8 * half);
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             wb[n] = st.b[(wn * 2 + n) * kWave + lane];
-                            sc[n] = mx_scale((st.bs[(wn * 2 + n) * kWave + lane] >> (8 * (kb & 3))) & 255u);
+                            sc[n] = mx_scale(((const uint8_t*)st.bs)[((wn * 2 + n) * kWave + lane) * 2 + (kb & 1)]);
                         }
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
@@ -275,14 +272,16 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
                         }
                     }
                 }
-                slot = slot == 2 ? 0 : slot + 1;
+                slot = slot == SLOTS - 1 ? 0 : slot + 1;
             }
         };
         if (RG == MI)
             stages(std::integral_constant<int, MI>{});
-        else if (MI > 2 && RG > 1)
-            stages(std::integral_constant<int, (MI > 2 ? MI - 1 : MI)>{});
-        else if (RG == 1)
+        else if (MI > 2 && RG == 3)
+            stages(std::integral_constant<int, (MI > 2 ? 3 : MI)>{});
+        else if (MI > 2 && RG == 2)
+            stages(std::integral_constant<int, (MI > 2 ? 2 : MI)>{});
+        else if (MI > 1 && RG == 1)
             stages(std::integral_constant<int, 1>{});
         else
             stages(std::integral_constant<int, 0>{});
@@ -323,34 +322,80 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
     wait_vm<0>();  // the loads past the last tile
 }
 
-template <bool A4, bool GATE_UP>
-hipError_t launch_mx(const MxGemmArgs& a, hipStream_t s)
+template <int BM, int WAVES_M, int SLOTS, bool A4, bool GATE_UP>
+hipError_t launch_shape(const MxGemmArgs& a, hipStream_t s)
 {
-    const int N = GATE_UP ? 2 * a.f : a.d;
-    const int S = GATE_UP ? 1 : a.split;
-    const int NT = (N + kBN - 1) / kBN;
-    if (a.small_tiles) {
-        const int64_t bound = ((int64_t)a.A_max / 64 + a.E) * NT * S;
-        const int grid = (int)std::min<int64_t>(bound, 2 * a.cus);
-        hipLaunchKernelGGL((mx_gemm_kernel<64, 1, A4, GATE_UP>), dim3(grid), dim3(4 * kWave), 0, s, a);
-    } else {
-        const int64_t bound = ((int64_t)a.A_max / 256 + a.E) * NT * S;
-        const int grid = (int)std::min<int64_t>(bound, a.cus);
-        hipLaunchKernelGGL((mx_gemm_kernel<256, 2, A4, GATE_UP>), dim3(grid), dim3(8 * kWave), 0, s, a);
-    }
+    const int NT = ((GATE_UP ? 2 * a.f : a.d) + kBN - 1) / kBN;
+    const int64_t tiles = ((int64_t)a.A_max / BM + a.E) * NT * (GATE_UP ? 1 : a.split);  // at most
+    const int grid = (int)std::min<int64_t>(tiles, WAVES_M == 1 ? 2 * a.cus : a.cus);
+    hipLaunchKernelGGL((mx_gemm_kernel<BM, WAVES_M, SLOTS, A4, GATE_UP>), dim3(grid), dim3(WAVES_M * 4 * kWave), 0, s,
+                       a);
     return hipGetLastError();
+}
+
+// Rows per tile from the mean rows per expert (the routing is on the device).
+// A tile costs its weights' stages whatever rows it holds, and its multiplied
+// row groups; an expert with a few rows more than the tile pays for two.
+// Measured (gate/up GEMM, us, tiles of 32 / 64 / 128 / 256 rows), bf16 rows:
+// 8 experts of 4096 x 14336 with 8 rows on average 97 / 98 / 105 / 139, 32 rows
+// 140 / 112 / 115 / 154, 83 rows 220 / 178 / 164 / 201, 1024 rows 2044 / 1595 /
+// 1496 / 1478; 128 of 2048 x 768 with 10 rows 44 / 44 / 46 / 59, 64 rows 96 / 73 /
+// 67 / 83. 4-bit rows: 8 rows 93 / 94 / 96 / 94, 250 rows 551 / 317 / 219 / 230,
+// 1024 rows 1356 / 951 / 713 / 671.
+int mx_tile_rows(int A, int E, bool a4)
+{
+    const int64_t mean = ((int64_t)A + E - 1) / E;
+    if (mean <= 20 && !a4)
+        return 32;
+    if (mean <= 40)
+        return 64;
+    return mean >= 400 && a4 ? 256 : 128;
 }
 
 }  // namespace
 
+int mx_down_split(int A, int E, int d, int f, int cus)
+{
+    // K splits of the down GEMM: up to four, until there are three tiles per
+    // compute unit (two run there at a time), while each part keeps 1024 k.
+    // Measured with one / two / four (down GEMM and combine, us): 8 experts of
+    // 4096 x 14336, 32 tokens - / 58 / 59, 333 tokens - / 103 / 96, 2047 tokens
+    // 470 / 454 / 483, 4096 tokens 842 / 859 / -; 128 experts of 2048 x 768 lose
+    // by every split (16 tokens 22 / 24).
+    const int rows = mx_tile_rows(A, E, false);
+    const int64_t mt = std::max<int64_t>(((int64_t)A + rows - 1) / rows, std::min(A, E));
+    const int64_t tiles = mt * ((d + kBN - 1) / kBN);
+    int s = 1;
+    while (s < kMxMaxSplit && tiles * s < 3 * (int64_t)cus && f / (2 * s) >= 1024)
+        s *= 2;
+    return s;
+}
+
+int64_t mx_split_rows(int cus)
+{
+    return (int64_t)128 * 3 * cus;  // then tiles of 128 rows make three per compute unit
+}
+
 hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s)
 {
-    return a.a_scales ? launch_mx<true, true>(a, s) : launch_mx<false, true>(a, s);
+    if (a.a_scales) {
+        const int rows = mx_tile_rows(a.A_max, a.E, true);
+        return rows == 64    ? launch_shape<64, 1, 3, true, true>(a, s)
+               : rows == 128 ? launch_shape<128, 1, 3, true, true>(a, s)
+                             : launch_shape<256, 2, 3, true, true>(a, s);
+    }
+    const int rows = mx_tile_rows(a.A_max, a.E, false);
+    return rows == 32   ? launch_shape<32, 1, 5, false, true>(a, s)
+           : rows == 64 ? launch_shape<64, 1, 4, false, true>(a, s)
+                        : launch_shape<128, 1, 3, false, true>(a, s);
 }
 
 hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s)
 {
-    return launch_mx<false, false>(a, s);
+    const int rows = mx_tile_rows(a.A_max, a.E, false);
+    return rows == 32   ? launch_shape<32, 1, 5, false, false>(a, s)
+           : rows == 64 ? launch_shape<64, 1, 4, false, false>(a, s)
+                        : launch_shape<128, 1, 3, false, false>(a, s);
 }
 
 }  // namespace cmoe

@@ -78,13 +78,21 @@ __device__ __forceinline__ bf16x8 mx8_to_bf16(uint32_t w, float sc)
 // +32, one scale block. That is the operand order of
 // v_mfma_scale_f32_32x32x64_f8f6f4 on 4-bit codes; turned into bf16, the
 // lane's word s (8 codes, k + 8 s) is its fragment of a 16-wide MFMA k step,
-// for which the activations are read in the same k order. The scale bytes of
-// four consecutive blocks stand together: word l of group (e, nb, kb/4) holds
-// lane l's byte of block kb in bits 8 (kb%4) .. +8, groups of 256 bytes,
-// mx_scale_groups(K) of them per 32 rows.
-__host__ __device__ __forceinline__ int mx_scale_groups(int K)
+// for which the activations are read in the same k order. The scale bytes
+// stand apart, 1 KiB per 256 rows x 128 k (what a GEMM tile takes in one load
+// per wave): byte mx_scale_at(...) is that of lane l's codes in block kb.
+__host__ __device__ __forceinline__ int mx_scale_tiles(int N)
 {
-    return (K / 64 + 3) / 4;
+    return (N + 255) / 256;
+}
+// Start of the 1 KiB of expert e's 32-row blocks 8 (nb/8) .. +8 at k unit u = kb/2.
+__host__ __device__ __forceinline__ int64_t mx_scale_group(int64_t e, int nb, int u, int N, int K)
+{
+    return ((e * mx_scale_tiles(N) + nb / 8) * (K / 128) + u) * 1024;
+}
+__host__ __device__ __forceinline__ int mx_scale_at(int nb, int kb, int l)
+{
+    return (nb % 8) * 128 + l * 2 + (kb & 1);
 }
 
 }  // namespace cmoe

@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint32_t*
 __global__ __launch_bounds__(kThreads) void mx_pack_blocked_kernel(const uint16_t* w0, const uint16_t* w1, Vec16* out,
                                                                    uint8_t* scales, int E, int N, int K)
 {
-    const int NB = N / 32, KB = K / 64, KG = mx_scale_groups(K);
+    const int NB = N / 32, KB = K / 64;
     const int64_t total = (int64_t)E * NB * KB * kWave;
     const int Nsrc = w1 ? N / 2 : N;
     for (int64_t idx = blockIdx.x * (int64_t)kThreads + threadIdx.x; idx < total;
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void mx_pack_blocked_kernel(const uint16_
         for (int q = 0; q < 4; ++q)
             c[q] = b == kMxNan ? 0u : mx_encode8(v[q], inv);
         out[idx] = c;
-        scales[((rb * KG + kb / 4) * kWave + l) * 4 + kb % 4] = (uint8_t)b;
+        scales[mx_scale_group(e, nb, kb / 2, N, K) + mx_scale_at(nb, kb, l)] = (uint8_t)b;
     }
 }
 
@@ -247,7 +247,7 @@ size_t mx_weight_bytes(int64_t E, int64_t N, int64_t K)
 
 size_t mx_weight_scale_bytes(int64_t E, int64_t N, int64_t K)
 {
-    return (size_t)(E * (N / 32) * mx_scale_groups((int)K) * kWave * 4);
+    return (size_t)(E * mx_scale_tiles((int)N) * (K / 128) * 1024);
 }
 
 hipError_t launch_mx_pack_blocked(const void* w0, const void* w1, void* out, uint8_t* scales, int E, int N, int K,
