@@ -76,6 +76,9 @@ struct colibri_moe {
     bool q4;      // and token rows for the gate/up GEMM
     Workspace ws; // in the arena, sized for max_tokens
     uint16_t* few_h;  // h of colibri_moe_forward_few [2][few tokens * k][f], bf16 layers
+    int few_split;      // parts of its down kernel's sums,
+    float* few_part;    // their sums [d/32][few_split][512]
+    int32_t* few_count; // and arrivals per 32 columns [d/32], zero between calls
     int32_t* ccnt;  // fused combine: arrivals per token and 128-column tile [max_tokens][d/128], zero between calls
     bool timing;
     hipEvent_t ev[kStages + 1];
@@ -300,7 +303,11 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     const size_t o_sd = h->fp8 ? cv.take(E * d * sizeof(float)) : 0;
     const size_t o_ccnt = h->fuse_combine ? cv.take((size_t)c.max_tokens * (d / 128) * sizeof(int32_t)) : 0;
     const size_t few_rows = (size_t)std::min(c.max_tokens, (int32_t)COLIBRI_MOE_FEW_TOKENS) * c.top_k;
-    const size_t o_few = c.dtype == COLIBRI_MOE_BF16 ? cv.take(2 * few_rows * f * sizeof(uint16_t)) : 0;
+    const bool few = c.dtype == COLIBRI_MOE_BF16;
+    const size_t o_few = few ? cv.take(2 * few_rows * f * sizeof(uint16_t)) : 0;
+    h->few_split = few ? few_down_split((int)d, h->cus) : 1;
+    const size_t o_fpart = few ? cv.take(d / 32 * h->few_split * 512 * sizeof(float)) : 0;
+    const size_t o_fcount = few ? cv.take(d / 32 * sizeof(int32_t)) : 0;
     const size_t o_ws = cv.take(layout_workspace(h, c.max_tokens, true, nullptr, nullptr));
     h->arena_bytes = cv.off;
 
@@ -319,12 +326,16 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     h->m_gu = h->mx4 ? base + o_mgu : nullptr;
     h->m_d = h->mx4 ? base + o_md : nullptr;
     h->ccnt = h->fuse_combine ? (int32_t*)(base + o_ccnt) : nullptr;
-    h->few_h = c.dtype == COLIBRI_MOE_BF16 ? (uint16_t*)(base + o_few) : nullptr;
+    h->few_h = few ? (uint16_t*)(base + o_few) : nullptr;
+    h->few_part = few ? (float*)(base + o_fpart) : nullptr;
+    h->few_count = few ? (int32_t*)(base + o_fcount) : nullptr;
     layout_workspace(h, c.max_tokens, true, base + o_ws, &h->ws);
 
     hipStream_t s = h->stream;
     if (h->ccnt)
         CMOE_HIP(hipMemsetAsync(h->ccnt, 0, (size_t)c.max_tokens * (d / 128) * sizeof(int32_t), s));
+    if (few)
+        CMOE_HIP(hipMemsetAsync(h->few_count, 0, d / 32 * sizeof(int32_t), s));
     CMOE_HIP(launch_transpose_router(w->w_router, h->w_rt, (int)d, (int)E, (int)es, s));
     if (w->b_router)
         CMOE_HIP(hipMemcpyAsync(h->b_r, w->b_router, E * sizeof(float), hipMemcpyDeviceToDevice, s));
@@ -720,6 +731,9 @@ colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, in
     a.inv = ro.inv;
     a.h = h->few_h;
     a.y = y;
+    a.split = h->few_split;
+    a.part = h->few_part;
+    a.count = h->few_count;
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[0], s));
     if (a.routed) {
@@ -735,7 +749,7 @@ colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, in
         CMOE_HIP(hipEventRecord(h->ev[3], s));
         CMOE_HIP(hipEventRecord(h->ev[4], s));
     }
-    CMOE_HIP(launch_few_down(a, h->cus, s));
+    CMOE_HIP(launch_few_down(a, s));
     if (tm) {
         CMOE_HIP(hipEventRecord(h->ev[5], s));
         CMOE_HIP(hipEventRecord(h->ev[6], s));

@@ -275,12 +275,17 @@ struct FewArgs {
     int32_t* inv;
     uint16_t* h;           // [2][T*k][f] bf16: high and low parts
     void* y;               // [T][d] bf16
+    int split;             // parts of the down kernel's sums (few_down_split)
+    float* part;           // split > 1: [d/32][split][512] their sums
+    int32_t* count;        // [d/32] parts finished, zero between calls
 };
+constexpr int kFewMaxSplit = 8;
+int few_down_split(int d, int cus);
 // Whether the first launch computes the routing (else launch_router_bf16 runs
 // before it).
 bool few_routes_itself(int d, int E);
 hipError_t launch_few_gate_up(const FewArgs& a, int cus, hipStream_t s);
-hipError_t launch_few_down(const FewArgs& a, int cus, hipStream_t s);
+hipError_t launch_few_down(const FewArgs& a, hipStream_t s);
 
 struct CombineArgs {
     const float* ys;    // split partials, each [A][d] fp32 by sorted position (ys_bf16: one [A][d] bf16)

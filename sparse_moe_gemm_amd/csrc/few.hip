@@ -52,7 +52,7 @@ struct Unit {
     static constexpr int K = 32 * M;
     static constexpr int kCG = FMT == kMx4 ? 2 : 1;  // gate/up: 16-column groups per item
     static constexpr int kXU = kXV / M;              // units of token fragments kept
-    static constexpr int kUPS = FMT == kMx4 ? 1 : 4; // units per step
+    static constexpr int kUPS = FMT == kBf16 ? 4 : FMT == kFp8 ? 2 : 1;  // units per step
 };
 
 // Byte offset of lane l's 16 bytes for rows 16 cj .. +16 of a 32-row block from
@@ -331,10 +331,6 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
         else
             route<8>(g, lds, r, first);
     }
-    const int nact = build_routes(r, g.T, g.k);
-    if (blockIdx.x == 0)
-        store_routes(g, r);
-
     // Token fragments of units wv + 16 i, i < XU, of K chunk ch.
     const int NU = g.d / U::K;
     const uint16_t* xr = (const uint16_t*)g.x + (int64_t)min(lane & 15, g.T - 1) * g.d + (lane >> 4) * (8 * M);
@@ -348,6 +344,8 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
             for (int s = 0; s < M; ++s)
                 x[i * M + s] = *(const Vec16*)(xr + u * U::K + s * 8);
         }
+    };
+    auto round_x = [&]() {
         if constexpr (FMT == kFp8) {
             if (g.act_quant)
 #pragma unroll
@@ -373,6 +371,11 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
                 }
         }
     };
+    load_x(0);  // on their way while the routes are built
+    const int nact = build_routes(r, g.T, g.k);
+    if (blockIdx.x == 0)
+        store_routes(g, r);
+
     if constexpr (FMT == kFp8) {
         if (g.act_quant) {  // the row's largest magnitude, over the lanes and waves that hold it
             uint32_t m = 0;
@@ -397,10 +400,10 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
     }
 
     // Steps of an item: UPS units per wave each. One where the units fit, else
-    // an even number for bf16 (two steps to a chunk of kept fragments).
+    // an even number (two steps to a chunk of kept fragments).
     const int P = NU <= kWaves * UPS ? 1 : (NU + kWaves * XU - 1) / (kWaves * XU) * (XU / UPS);
     const bool one_chunk = NU <= kWaves * XU;
-    load_x(0);
+    round_x();
     const int groups = g.f / (16 * CG);
     const int items = nact * groups;
     const int mine = (int)blockIdx.x < items ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
@@ -467,8 +470,10 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
     // Step q from set t; the item's sums leave after its last step.
     auto take = [&](const Step<FMT>& t, int q) {
         const int p = q % P;
-        if (!one_chunk && p % (XU / UPS) == 0)
+        if (!one_chunk && p % (XU / UPS) == 0) {
             load_x(p / (XU / UPS));
+            round_x();
+        }
         if (XU / UPS == 1 || (p & 1) == 0)
             multiply(t, p, std::integral_constant<int, 0>{});
         else
@@ -523,29 +528,37 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
     }
 }
 
-// Loads of B units of the down kernel: weights, scales, and the token
-// fragments of h (high and low parts; lanes whose token did not choose the
-// expert load nothing and hold zeros).
-template <int FMT, int B>
+// Loads of B units of the down kernel: weights and scales of both 16-row
+// halves, and the token fragments of h (lanes whose token did not choose the
+// expert load nothing and hold zeros). H = 2: high and low parts apart, for 16
+// tokens; H = 1: at most 8 tokens, whose high parts are columns 0..7 and low
+// parts columns 8..15 of one fragment.
+template <int FMT, int B, int H>
 struct DownStep {
     static constexpr int M = Unit<FMT>::M;
-    Vec16 w[B];
-    uint32_t mx[FMT == kMx4 ? B : 1];
-    float sc[FMT == kFp8 ? B : 1];
-    Vec16 hi[B][M], lo[B][M];
+    Vec16 w[B][2];
+    uint32_t mx[FMT == kMx4 ? B : 1][2];
+    float sc[FMT == kFp8 ? B : 1][2];
+    Vec16 x[B][M][H];
     float wt[B];  // routing weight, -1 if the lane's token did not choose the expert
 };
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-template <int FMT>
+// A work item is 32 output columns (both halves of a row block: an h
+// fragment costs as much to load as a weight one, so each serves two, and up to
+// 8 tokens take one fragment instead of two: 7 tokens on 4-bit weights
+// 77 -> 56 us with both halves) and one of g.split parts of the units of all active experts, which its 16 waves take
+// in interleaved order. With more than one part the parts' sums go to memory
+// and the workgroup that finishes the column block last adds them in the order
+// of the parts: nobody waits, and the result does not depend on who is last.
+template <int FMT, int H>
 __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
 {
     using U = Unit<FMT>;
     constexpr int M = U::M;
-    constexpr int B = FMT == kBf16 ? 3 : FMT == kFp8 ? 2 : 1;
+    constexpr int B = FMT == kBf16 ? (H == 1 ? 4 : 3) : FMT == kFp8 && H == 1 ? 2 : 1;
     __shared__ Routes r;
-    __shared__ float red[kWaves][256];
+    __shared__ __align__(16) float red[kWaves][512];
+    __shared__ int last;
 
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -555,82 +568,160 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
         r.w[tid] = g.w[tid];
     }
     const int nact = build_routes(r, g.T, g.k);
-    const int NU = g.f / U::K;   // units per expert
-    const int V = nact * NU;     // of the item, over its experts
+    const int NU = g.f / U::K;  // units per expert
     const int KB = 2 * NU, NBK = g.d / 32;
     const uint32_t plane = (uint32_t)A * (uint32_t)g.f * 2u;
     const __amdgpu_buffer_rsrc_t rh = __builtin_amdgcn_make_buffer_rsrc((void*)g.h, 0, (int)(2 * plane), 0x00020000);
+    const uint32_t lane_w = unit_lane(0, lane), lane_m = unit_scale_lane(0, lane);
 
-    for (int n = blockIdx.x; n < g.d / 16; n += gridDim.x) {
-        const uint32_t lane_w = unit_lane(n & 1, lane), lane_m = unit_scale_lane(n & 1, lane);
-        floatx4 total = {0.f, 0.f, 0.f, 0.f};
-        auto load = [&](DownStep<FMT, B>& t, int i0) {
+    const int nb = (int)blockIdx.x / g.split, part = (int)blockIdx.x - nb * g.split;
+    const int v0 = (int)((int64_t)part * nact * NU / g.split);
+    const int V = (int)((int64_t)(part + 1) * nact * NU / g.split);  // units v0 .. V of the item
+    floatx4 total[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // The wave's next unit to load: unit cu of active expert ca, of whose
+    // tokens and weights cwt, crow, cw, cm, cs tell.
+    int cv = v0 + wv, ca = -1, cu = 0;
+    float cwt = 0.f, cs[2] = {1.f, 1.f};
+    uint32_t crow = 0;
+    const uint8_t *cw = nullptr, *cm = nullptr;
+    auto open = [&](int a) {
+        ca = a;
+        const int e = __builtin_amdgcn_readfirstlane(r.act[a]);
+        const int64_t rb = (int64_t)e * NBK + nb;
+        const Choice ch = r.tab[a][H == 1 ? lane & 7 : lane & 15];
+        cwt = ch.row < 0 ? -1.f : ch.w;
+        // past the buffer for lanes that hold zeros
+        crow = ch.row < 0 ? 0x80000000u : ((uint32_t)ch.row * (uint32_t)g.f + (uint32_t)((lane >> 4) * 8 * M)) * 2u;
+        if (H == 1 && (lane & 8))
+            crow += plane;
+        cw = uniform((const uint8_t*)g.w_d + rb * KB * 1024);
+        if constexpr (FMT == kMx4)
+            cm = uniform(g.m_d + mx_scale_group(e, nb, 0, g.d, g.f) + mx_scale_at(nb, 0, 0));
+        if constexpr (FMT == kFp8)
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int v = min(wv + kWaves * (i0 + b), V - 1);
-                const int a = v / NU, u = v - a * NU;
-                const int e = __builtin_amdgcn_readfirstlane(r.act[a]);
-                const int64_t rb = (int64_t)e * NBK + n / 2;
-                const Choice ch = r.tab[a][lane & 15];
-                t.wt[b] = ch.row < 0 ? -1.f : ch.w;
-                t.w[b] = __builtin_nontemporal_load(
-                    (const Vec16*)(uniform((const uint8_t*)g.w_d + (rb * KB + 2 * u) * 1024) + lane_w));
+            for (int h = 0; h < 2; ++h)
+                cs[h] = ((const float*)uniform(g.s_d + rb * 32))[16 * h + (lane & 15)];
+    };
+    auto load = [&](DownStep<FMT, B, H>& t) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            t.wt[b] = cwt;
+            const uint8_t* wp = cw + (int64_t)cu * 2048;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                t.w[b][h] = __builtin_nontemporal_load((const Vec16*)(wp + lane_w + h * 256));
                 if constexpr (FMT == kMx4)
-                    t.mx[b] = uniform(g.m_d + mx_scale_group(e, n / 2, u, g.d, g.f) + mx_scale_at(n / 2, 0, 0))[lane_m];
+                    t.mx[b][h] = (cm + (int64_t)cu * 1024)[lane_m + h * 32];
                 if constexpr (FMT == kFp8)
-                    t.sc[b] = g.s_d[rb * 32 + 16 * (n & 1) + (lane & 15)];
-                // past the buffer for lanes that hold zeros
-                const uint32_t at = ch.row < 0 ? 0x80000000u
-                                               : ((uint32_t)ch.row * (uint32_t)g.f + (uint32_t)(u * U::K) +
-                                                  (uint32_t)((lane >> 4) * 8 * M)) * 2u;
-#pragma unroll
-                for (int s = 0; s < M; ++s) {
-                    t.hi[b][s] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(at + 16u * s), 0, 0));
-                    t.lo[b][s] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(at + 16u * s), (int)plane, 0));
-                }
+                    t.sc[b][h] = cs[h];
             }
-        };
-        auto multiply = [&](const DownStep<FMT, B>& t, int i0) {
+            const int at = cu * U::K * 2;
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                if (wv + kWaves * (i0 + b) >= V)
-                    continue;
-                floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-                const float sc = FMT == kMx4 ? mx_scale(t.mx[FMT == kMx4 ? b : 0]) : t.sc[FMT == kFp8 ? b : 0];
+            for (int s = 0; s < M; ++s)
 #pragma unroll
-                for (int s = 0; s < M; ++s) {
-                    const bf16x8 f = unit_frag<FMT>(t.w[b], s, sc);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(t.lo[b][s]), acc, 0, 0, 0);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(t.hi[b][s]), acc, 0, 0, 0);
+                for (int h = 0; h < H; ++h)
+                    t.x[b][s][h] = __builtin_bit_cast(
+                        Vec16, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(crow + 16u * s), at + h * (int)plane, 0));
+            if (cv + kWaves < V) {  // else this unit again, not multiplied
+                cv += kWaves;
+                cu += kWaves;
+                int a = ca;
+                while (cu >= NU) {
+                    cu -= NU;
+                    ++a;
                 }
-                // only the tokens that chose this expert take its rows (whose
-                // weights may be infinite or NaN)
+                if (a != ca)
+                    open(a);
+            }
+        }
+    };
+    auto multiply = [&](const DownStep<FMT, B, H>& t, int i0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (v0 + wv + kWaves * (i0 + b) >= V)
+                continue;
+            floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int s = 0; s < M; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float sc = FMT == kMx4 ? mx_scale(t.mx[FMT == kMx4 ? b : 0][h]) : t.sc[FMT == kFp8 ? b : 0][h];
+                    const bf16x8 f = unit_frag<FMT>(t.w[b][h], s, sc);
+#pragma unroll
+                    for (int p = 0; p < H; ++p)
+                        acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(t.x[b][s][p]), acc[h], 0, 0, 0);
+                }
+            // only the tokens that chose this expert take its rows (whose
+            // weights may be infinite or NaN)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    total[i] = t.wt[b] < 0.f ? total[i] : fmaf(t.wt[b], acc[i], total[i]);
-            }
-        };
-        const int I = (V + kWaves - 1) / kWaves;  // units per wave, at most
-        DownStep<FMT, B> t0, t1;
-        load(t0, 0);
+                    total[h][i] = t.wt[b] < 0.f ? total[h][i] : fmaf(t.wt[b], acc[h][i], total[h][i]);
+        }
+    };
+    const int I = (V - v0 + kWaves - 1) / kWaves;  // units per wave, at most
+    if (cv < V) {
+        cu = cv;
+        int a = 0;
+        while (cu >= NU) {
+            cu -= NU;
+            ++a;
+        }
+        open(a);
+        DownStep<FMT, B, H> t0, t1;
+        load(t0);
         for (int i = 0; i < I; i += 2 * B) {
-            load(t1, i + B);
+            load(t1);
             multiply(t0, i);
-            load(t0, i + 2 * B);
+            load(t0);
             multiply(t1, i + B);
         }
-        *(floatx4*)(&red[wv][lane * 4]) = total;
-        lds_barrier();
-        if (tid < 256) {
-            float s = 0.f;
+    }
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                s += red[w][tid];
-            const int t = (tid / 4) % 16, col = n * 16 + 4 * (tid / 64) + tid % 4;
-            if (t < g.T)
-                ((uint16_t*)g.y)[(int64_t)t * g.d + col] = f32_to_bf16_bits(s);
-        }
+    for (int h = 0; h < 2; ++h)
+        *(floatx4*)(&red[wv][h * 256 + lane * 4]) = total[h];
+    lds_barrier();
+    float sum = 0.f;
+    if (tid < 512)
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            sum += H == 1 ? red[w][tid] + red[w][tid ^ 32] : red[w][tid];  // ^ 32: eight columns on
+    if (g.split > 1) {
+        // Parts and counts are accessed at device scope (written through and
+        // read past the XCDs' separate L2s), ordered by the wait for the stores
+        // and the barrier before the count. Fences would do the same by
+        // flushing every L2 from every wave, which took 115 us here.
+        float* mine = g.part + (int64_t)blockIdx.x * 512;
+        if (tid < 512)
+            __hip_atomic_store(mine + tid, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
+        if (tid == 0)
+            last = __hip_atomic_fetch_add(&g.count[nb], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == g.split - 1;
+        lds_barrier();
+        if (!last)
+            return;
+        if (tid == 0)  // for the next call
+            __hip_atomic_store(&g.count[nb], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        float v[kFewMaxSplit];
+        sum = 0.f;
+        if (tid < 512) {
+#pragma unroll
+            for (int p = 0; p < kFewMaxSplit; ++p)
+                if (p < g.split)
+                    v[p] = __hip_atomic_load(g.part + ((int64_t)nb * g.split + p) * 512 + tid, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int p = 0; p < kFewMaxSplit; ++p)
+                if (p < g.split)
+                    sum += v[p];
+        }
+    }
+    if (tid < 512) {
+        const int el = tid % 256, t = (el / 4) % 16, col = nb * 32 + tid / 256 * 16 + 4 * (el / 64) + el % 4;
+        if (t < g.T)
+            ((uint16_t*)g.y)[(int64_t)t * g.d + col] = f32_to_bf16_bits(sum);
     }
 }
 
@@ -653,15 +744,20 @@ hipError_t launch_few_gate_up(const FewArgs& a, int cus, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_few_down(const FewArgs& a, int cus, hipStream_t s)
+int few_down_split(int d, int cus)
 {
-    const dim3 grid(std::min(cus, a.d / 16)), block(kThreads);
-    if (a.m_gu)
-        hipLaunchKernelGGL(few_down_kernel<kMx4>, grid, block, 0, s, a);
-    else if (a.s_gu)
-        hipLaunchKernelGGL(few_down_kernel<kFp8>, grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL(few_down_kernel<kBf16>, grid, block, 0, s, a);
+    // A workgroup per compute unit, in at most kFewMaxSplit parts: reading the
+    // weights at full rate takes them all.
+    return std::max(1, std::min(kFewMaxSplit, cus / (d / 32)));
+}
+
+hipError_t launch_few_down(const FewArgs& a, hipStream_t s)
+{
+    const dim3 grid(a.d / 32 * a.split), block(kThreads);
+    auto k = a.m_gu   ? (a.T <= 8 ? few_down_kernel<kMx4, 1> : few_down_kernel<kMx4, 2>)
+             : a.s_gu ? (a.T <= 8 ? few_down_kernel<kFp8, 1> : few_down_kernel<kFp8, 2>)
+                      : (a.T <= 8 ? few_down_kernel<kBf16, 1> : few_down_kernel<kBf16, 2>);
+    hipLaunchKernelGGL(k, grid, block, 0, s, a);
     return hipGetLastError();
 }
 
