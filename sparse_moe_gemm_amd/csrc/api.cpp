@@ -25,7 +25,6 @@ namespace {
 constexpr uint32_t kMagic = 0xC011B41Eu;
 constexpr int kStages = 6;
 constexpr int32_t kMaxTokensLimit = 1 << 24;
-constexpr size_t kMxBlockValues = 32;  // values per scale byte of the 4-bit format
 static_assert(COLIBRI_MOE_FEW_TOKENS == kFewTokens, "header and kernels agree");
 
 const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_up_gemm",
@@ -37,9 +36,9 @@ const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_u
 // buffers the caller did not supply, H, the fp32 partial sums, and the 8-bit
 // token rows of the W8A8 mode.
 struct Workspace {
-    uint8_t* xq;  // q8: token rows as E4M3 codes [T][d]; q4: as E2M1 codes [T][d/2]
+    uint8_t* xq;  // q8: token rows as E4M3 codes [T][d]; q4: 4-bit rows by sorted position (mxfp4.hpp)
     float* xsc;   // q8: their scales by sorted position [A]
-    uint8_t* xsb; // q4: their scale bytes [T][d/32]
+    uint8_t* xsb; // q4: their scale bytes
     float* topw;
     int32_t* ids;
     int32_t* counts;
@@ -237,9 +236,9 @@ size_t layout_workspace(const colibri_moe* h, int64_t T, bool up_to, uint8_t* ba
     const size_t d = c.d_model, f = c.d_ff, E = c.n_experts, k = c.top_k;
     const size_t A = (size_t)T * k;
     Carver cv;
-    const size_t o_xq = h->q8 ? cv.take((size_t)T * d) : h->q4 ? cv.take((size_t)T * d / 2) : 0;
+    const size_t o_xq = h->q8 ? cv.take((size_t)T * d) : h->q4 ? cv.take(mx_row_bytes((int)A, (int)E, (int)d)) : 0;
     const size_t o_xsc = h->q8 ? cv.take(A * sizeof(float)) : 0;
-    const size_t o_xsb = h->q4 ? cv.take((size_t)T * d / kMxBlockValues) : 0;
+    const size_t o_xsb = h->q4 ? cv.take(mx_row_scale_bytes((int)A, (int)E, (int)d)) : 0;
     const size_t o_topw = cv.take(A * sizeof(float));
     const size_t o_ids = cv.take(A * sizeof(int32_t));
     const size_t o_cnt = cv.take(E * sizeof(int32_t));
@@ -517,7 +516,7 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
         CMOE_HIP(launch_act_quant(x, T, c.d_model, c.top_k, inv, ws.xq, ws.xsc, s));
     const bool mx4 = h->mx4, q4 = h->q4;
     if (q4)  // token rows to 4 bits
-        CMOE_HIP(launch_mx_quantize(x, 1, T, c.d_model, c.d_model, ws.xq, ws.xsb, s));
+        CMOE_HIP(launch_mx_quantize_sorted(x, offsets, perm, T * c.top_k, c.n_experts, c.d_model, ws.xq, ws.xsb, s));
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[2], s));
 

@@ -220,6 +220,12 @@ hipError_t launch_mx_quantize(const void* w, int bf16_in, int64_t rows, int64_t 
                               uint8_t* scales, hipStream_t s);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int bf16_out,
                                 void* out, hipStream_t s);
+// Token rows of a forward with A = T*k assignments in the tiled GEMM's blocked
+// layout, by sorted position, and the sizes of its two parts.
+hipError_t launch_mx_quantize_sorted(const void* x, const int32_t* offsets, const int32_t* perm, int A, int E, int d,
+                                     uint8_t* codes, uint8_t* scales, hipStream_t s);
+size_t mx_row_bytes(int A, int E, int d);
+size_t mx_row_scale_bytes(int A, int E, int d);
 // bf16 expert weights [E][N][K] (w1: gate/up interleaved by 32 rows) in the
 // GEMM layout, and the sizes of its two parts.
 size_t mx_weight_bytes(int64_t E, int64_t N, int64_t K);
@@ -229,8 +235,8 @@ hipError_t launch_mx_pack_blocked(const void* w0, const void* w1, void* out, uin
 
 // Tiled grouped GEMMs on 4-bit weights (gemm_mxfp4.hip).
 struct MxGemmArgs {
-    const void* a;            // gate/up: x [T][d] bf16, or its codes; down: H [A][f] bf16
-    const uint8_t* a_scales;  // gate/up on 4-bit token rows: scale bytes [T][d/32]; else null
+    const void* a;            // gate/up: x [T][d] bf16, or blocked 4-bit rows; down: H [A][f] bf16
+    const uint8_t* a_scales;  // gate/up on 4-bit token rows: their scales; else null
     const void* b;            // weight codes and scales in the GEMM layout
     const uint8_t* b_scales;
     void* out;                // gate/up: H [A][f] bf16; down: fp32 partials [split][A][d]

@@ -47,25 +47,23 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b)
     return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
 }
 
-// One K stage: BM token rows of RB bytes (64 k as bf16, 128 k as codes), their
-// scale words (A4: bytes of the row's four blocks), KBS 1 KiB weight blocks
-// for each 32 weight rows and the scales of the 128 k they belong to.
+// One K stage: the token rows (64 k of BM bf16 rows, 128 bytes each; or 128 k of
+// 4-bit rows, which come blocked as the weights do), KBS 1 KiB weight blocks
+// for each 32 weight rows, and the scales of the 128 k they belong to.
 template <int BM, bool A4>
 struct MxStage {
-    static constexpr int RB = A4 ? 64 : 128;
     static constexpr int KBS = A4 ? 2 : 1;
-    Vec16 a[BM * RB / 16];
+    Vec16 a[A4 ? BM / 32 * 2 * kWave : BM * 8];
     Vec16 b[(kBN / 32) * KBS * kWave];
     uint16_t bs[(kBN / 32) * kWave];
-    uint32_t as[A4 ? (BM < kWave ? kWave : BM) : 4];
+    uint16_t as[A4 ? BM / 32 * kWave : 8];
 };
 
-// Position of 16-byte chunk c of tile row r in the stage: the 16 rows that 16
-// lanes read at one chunk fall into 16 different 16-byte bank groups.
-template <bool A4>
+// Position of 16-byte chunk c of bf16 tile row r in the stage: the 16 rows that
+// 16 lanes read at one chunk fall into 16 different 16-byte bank groups.
 __device__ __forceinline__ int mx_swz(int r, int c)
 {
-    return A4 ? (c ^ ((r >> 2) & 3)) : (c ^ ((r >> 1) & 7));
+    return c ^ ((r >> 1) & 7);
 }
 
 template <int BM, int WAVES_M, bool A4>
@@ -73,13 +71,12 @@ struct MxShape {
     using Stage = MxStage<BM, A4>;
     static constexpr int NW = WAVES_M * 4;
     static constexpr int WM = BM / WAVES_M;
-    static constexpr int ROWS = A4 ? 16 : 8;  // tile rows per 1 KiB load
     // Loads per wave and stage. Every wave issues as many (the waits count
     // them); where there are fewer loads than waves, waves share one and write
     // the same data to the same place.
-    static constexpr int A_ALL = BM / ROWS, A_INS = A_ALL < NW ? 1 : A_ALL / NW;
+    static constexpr int A_ALL = A4 ? BM / 16 : BM / 8, A_INS = A_ALL < NW ? 1 : A_ALL / NW;
     static constexpr int B_INS = (kBN / 32) * Stage::KBS / NW;
-    static constexpr int AS_ALL = BM < kWave ? 1 : BM / kWave;
+    static constexpr int AS_ALL = BM / kWave;  // A4
     static constexpr int NLD = A_INS + B_INS + 1 + (A4 ? 1 : 0);
     static_assert(B_INS >= 1, "every wave loads a share");
 };
@@ -89,8 +86,8 @@ struct MxShape {
 template <int A_INS>
 struct MxCursor {
     Rsrc rb, rs;           // the tile's weight blocks and scale groups
-    uint32_t aoff[A_INS];  // byte offsets of this lane's rows and chunk
-    uint32_t asoff;        // A4: byte offset of this lane's row of scales
+    Rsrc ra, ras;          // A4: its token blocks and their scales
+    uint32_t aoff[A_INS];  // bf16 rows: byte offsets of this lane's rows and chunk
     int kt, left;          // next stage along K, stages left in the tile
     int L;                 // the tile's launch index
 };
@@ -122,10 +119,13 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
     if ((int)blockIdx.x >= total)
         return;
 
-    const uint32_t Kbytes = A4 ? (uint32_t)K / 2 : (uint32_t)K * 2;
+    const uint32_t Kbytes = (uint32_t)K * 2;
     const uint32_t a_rows = GATE_UP ? (uint32_t)(g.A_max / g.k) : (uint32_t)g.A_max;
-    const Rsrc ra = buffer_rsrc(g.a, a_rows * Kbytes);
-    const Rsrc ras = buffer_rsrc(A4 ? (const void*)g.a_scales : g.a, A4 ? a_rows * (uint32_t)(K / 32) : 0u);
+    const Rsrc ra = buffer_rsrc(g.a, A4 ? 0u : a_rows * Kbytes);
+    const int MB = mx_row_blocks(g.A_max, g.E);
+    int blocks_below = 0;  // A4: 32-row blocks of the experts below this lane's four
+    if constexpr (A4)
+        blocks_below = mx_blocks_below(tt, lane);
     const uint32_t lane16 = (uint32_t)lane * 16u, lane4 = (uint32_t)lane * 4u;
     const uint32_t ring0 = lds_address(&ring[0]);
 
@@ -139,14 +139,17 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
         const int64_t blk = (int64_t)t.e * (N / 32) + nb0;
         c.rb = buffer_rsrc((const uint8_t*)g.b + blk * KB * 1024, (uint32_t)min(nbs, kBN / 32) * (uint32_t)KB * 1024u);
         c.rs = buffer_rsrc(g.b_scales + mx_scale_group(t.e, nb0, 0, N, K), (uint32_t)(K / 128) * 1024u);
+        if constexpr (A4) {
+            const int first = mx_block_of(tt, blocks_below, t.e) + t.m * (BM / 32), n = (t.rows + 31) / 32;
+            c.ra = buffer_rsrc((const uint8_t*)g.a + (int64_t)first * KB * 1024, (uint32_t)n * (uint32_t)KB * 1024u);
+            c.ras = buffer_rsrc(g.a_scales + (int64_t)first * 128, ((uint32_t)KT * (uint32_t)MB - (uint32_t)first) * 128u);
+        } else {
 #pragma unroll
-        for (int q = 0; q < Sh::A_INS; ++q) {
-            const int per = Sh::Stage::RB / 16;  // chunks per row
-            const int r = (wv * Sh::A_INS + q) % Sh::A_ALL * Sh::ROWS + lane / per;
-            c.aoff[q] = row_of(t, r) * Kbytes + (uint32_t)mx_swz<A4>(r, lane % per) * 16u;
+            for (int q = 0; q < Sh::A_INS; ++q) {
+                const int r = (wv * Sh::A_INS + q) % Sh::A_ALL * 8 + lane / 8;
+                c.aoff[q] = row_of(t, r) * Kbytes + (uint32_t)mx_swz(r, lane % 8) * 16u;
+            }
         }
-        if constexpr (A4)
-            c.asoff = row_of(t, (wv % Sh::AS_ALL) * kWave + lane) * (uint32_t)(K / 32);
         c.kt = t.kt0;
         c.left = t.nkt;
         c.L = L;
@@ -157,9 +160,14 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
     auto request = [&](MxCursor<Sh::A_INS>& c, int slot) {
         const uint32_t base = ring0 + (uint32_t)slot * (uint32_t)sizeof(Stage);
 #pragma unroll
-        for (int q = 0; q < Sh::A_INS; ++q)
-            lds_load16(ra, c.aoff[q], (uint32_t)c.kt * (uint32_t)Stage::RB,
-                       base + (uint32_t)offsetof(Stage, a) + (uint32_t)((wv * Sh::A_INS + q) % Sh::A_ALL) * 1024u);
+        for (int q = 0; q < Sh::A_INS; ++q) {
+            const int i = (wv * Sh::A_INS + q) % Sh::A_ALL;
+            const uint32_t to = base + (uint32_t)offsetof(Stage, a) + (uint32_t)i * 1024u;
+            if constexpr (A4)
+                lds_load16(c.ra, lane16, ((uint32_t)(i / 2) * (uint32_t)KB + (uint32_t)(c.kt * 2 + i % 2)) * 1024u, to);
+            else
+                lds_load16(ra, c.aoff[q], (uint32_t)c.kt * 128u, to);
+        }
 #pragma unroll
         for (int q = 0; q < Sh::B_INS; ++q) {
             const int i = wv * Sh::B_INS + q;  // row block i / KBS, k block i % KBS of the stage
@@ -170,7 +178,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
         lds_load4(c.rs, lane4, (uint32_t)(c.kt * Stage::KBS / 2) * 1024u + (uint32_t)(wv % 4) * 256u,
                   base + (uint32_t)offsetof(Stage, bs) + (uint32_t)(wv % 4) * 256u);
         if constexpr (A4)
-            lds_load4(ras, c.asoff, (uint32_t)c.kt * 4u,
+            lds_load4(c.ras, lane4 + (uint32_t)(wv % Sh::AS_ALL) * 256u, (uint32_t)c.kt * (uint32_t)MB * 128u,
                       base + (uint32_t)offsetof(Stage, as) + (uint32_t)(wv % Sh::AS_ALL) * 256u);
         if (c.left > 1) {
             ++c.kt;
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
                             sb[n] = st.bs[(wn * 2 + n) * kWave + lane];
 #pragma unroll
                         for (int i = 0; i < RGC; ++i)
-                            sa[i] = st.as[wm * Sh::WM + i * 32 + (lane & 31)] >> (8 * half);
+                            sa[i] = st.as[(wm * MI + i) * kWave + lane];
                         auto step = [&](auto s_const) {
                             constexpr int s = decltype(s_const)::value;
                             v8i fb[2], fa[RGC];
@@ -232,8 +240,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
                             }
 #pragma unroll
                             for (int i = 0; i < RGC; ++i) {
-                                const int r = wm * Sh::WM + i * 32 + (lane & 31);
-                                const Vec16 w = st.a[r * 4 + mx_swz<true>(r, 2 * s + half)];
+                                const Vec16 w = st.a[((wm * MI + i) * 2 + s) * kWave + lane];
                                 fa[i] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
                             }
 #pragma unroll
@@ -241,7 +248,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
                                 for (int n = 0; n < 2; ++n)
                                     acc[n][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                        fb[n], fa[i], acc[n][i], 4, 4, s, (int)sb[n], 2 * s, (int)sa[i]);
+                                        fb[n], fa[i], acc[n][i], 4, 4, s, (int)sb[n], s, (int)sa[i]);
                         };
                         step(std::integral_constant<int, 0>{});
                         step(std::integral_constant<int, 1>{});
@@ -259,7 +266,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
 #pragma unroll
                             for (int i = 0; i < RGC; ++i) {
                                 const int r = wm * Sh::WM + i * 32 + (lane & 31);
-                                fa[i] = as_bf16x8(st.a[r * 8 + mx_swz<false>(r, 4 * half + s)]);
+                                fa[i] = as_bf16x8(st.a[r * 8 + mx_swz(r, 4 * half + s)]);
                             }
 #pragma unroll
                             for (int n = 0; n < 2; ++n)

@@ -7,7 +7,7 @@
 // makes all 32 values NaN. Code 2i of a row is in the low half of byte i.
 #pragma once
 
-#include "common.hpp"
+#include "tiles.hpp"
 
 namespace cmoe {
 
@@ -93,6 +93,44 @@ __host__ __device__ __forceinline__ int64_t mx_scale_group(int64_t e, int nb, in
 __host__ __device__ __forceinline__ int mx_scale_at(int nb, int kb, int l)
 {
     return (nb % 8) * 128 + l * 2 + (kb & 1);
+}
+
+// Token rows in 4 bits for the tiled GEMM, by sorted position: every expert's
+// rows start a new 32-row block, blocks are numbered through the experts, at
+// most mx_row_blocks of them. Codes as the weights': block (b, kb) of 1 KiB at
+// (b * K/64 + kb) * 1024; scale bytes of block b and k unit u: 128 bytes at
+// (u * mx_row_blocks + b) * 128, lane l's two at 2 l.
+__host__ __device__ __forceinline__ int mx_row_blocks(int A, int E)
+{
+    return A / 32 + (A < E ? A : E);
+}
+
+// From a tile table: blocks of the experts below this lane's four, and an
+// expert's first block (e wave-uniform).
+__device__ __forceinline__ int mx_blocks_below(const TileTable& t, int lane)
+{
+    int own = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        own += (t.cnt[q] + 31) / 32;
+    int incl = own;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(incl, d, kWave);
+        if (lane >= d)
+            incl += o;
+    }
+    return incl - own;
+}
+
+__device__ __forceinline__ int mx_block_of(const TileTable& t, int below, int e)
+{
+    const int ln = e / 4;
+    int b = __builtin_amdgcn_readlane(below, ln);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        b += q < e % 4 ? (__builtin_amdgcn_readlane(t.cnt[q], ln) + 31) / 32 : 0;
+    return __builtin_amdgcn_readfirstlane(b);
 }
 
 }  // namespace cmoe

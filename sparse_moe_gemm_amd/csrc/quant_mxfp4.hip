@@ -189,6 +189,51 @@ __global__ __launch_bounds__(kThreads) void mx_pack_blocked_kernel(const uint16_
     }
 }
 
+// Token rows [T][d] of a forward into the blocked 4-bit layout of the tiled
+// GEMM (mxfp4.hpp), gathered by sorted position: a wave takes 32 rows x 128 k,
+// a lane one block of 32 values at a time, so the maximum needs no exchange and
+// codes leave as 1 KiB per store. Rows past an expert's last repeat it.
+__global__ __launch_bounds__(kThreads) void mx_quantize_sorted_kernel(const uint16_t* x, const int32_t* offsets,
+                                                                      const int32_t* perm, int A, int E, int d,
+                                                                      Vec16* codes, uint16_t* scales)
+{
+    const int lane = threadIdx.x % kWave;
+    const int MB = mx_row_blocks(A, E), KB = d / 64, KU = d / 128;
+    TileTable tt;
+    const int blocks = make_table<32>(offsets, E, lane, 1, tt);  // 32-row tiles are the blocks
+    const int W = gridDim.x * (kThreads / kWave);
+    const int w0 = blockIdx.x * (kThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    for (int it = w0; it < blocks * KU; it += W) {
+        const int b = it / KU, u = it - b * KU;
+        const Tile t = decode<32>(tt, b, 1, 1, 1, 1);
+        const int64_t row = perm[t.row0 + min(lane & 31, t.rows - 1)];
+        const uint16_t* p = x + row * d + u * 128 + 32 * (lane >> 5);
+        float v[2][4][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                load8<true>(p + 64 * h + 8 * q, v[h][q]);
+        uint32_t sb = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                m = max(m, amax_bits8(v[h][q]));
+            const uint32_t s = mx_scale_byte(m);
+            const float inv = mx_inv_scale(s == kMxNan ? 127u : s);
+            Vec16 c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                c[q] = s == kMxNan ? 0u : mx_encode8(v[h][q], inv);
+            codes[((int64_t)b * KB + 2 * u + h) * kWave + lane] = c;
+            sb |= s << (8 * h);
+        }
+        scales[((int64_t)u * MB + b) * kWave + lane] = (uint16_t)sb;
+    }
+}
+
 unsigned unit_blocks(int64_t units)
 {
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>((units + kThreads * kUnits - 1) / (kThreads * kUnits), 8192));
@@ -238,6 +283,26 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
     else
         hipLaunchKernelGGL(mx_dequantize_kernel<false>, grid, block, 0, s, (const uint32_t*)codes, scales, units, out);
     return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize_sorted(const void* x, const int32_t* offsets, const int32_t* perm, int A, int E, int d,
+                                     uint8_t* codes, uint8_t* scales, hipStream_t s)
+{
+    const int64_t waves = (int64_t)mx_row_blocks(A, E) * (d / 128);
+    const unsigned blocks = (unsigned)std::min<int64_t>((waves + 3) / 4, 4096);
+    hipLaunchKernelGGL(mx_quantize_sorted_kernel, dim3(blocks), dim3(kThreads), 0, s, (const uint16_t*)x, offsets, perm,
+                       A, E, d, (Vec16*)codes, (uint16_t*)scales);
+    return hipGetLastError();
+}
+
+size_t mx_row_bytes(int A, int E, int d)
+{
+    return (size_t)mx_row_blocks(A, E) * 32 * (d / 2);
+}
+
+size_t mx_row_scale_bytes(int A, int E, int d)
+{
+    return (size_t)mx_row_blocks(A, E) * d;
 }
 
 size_t mx_weight_bytes(int64_t E, int64_t N, int64_t K)
