@@ -172,14 +172,22 @@ def colibri_moe_dequantize_mxfp4(codes_ptr: int, scales_ptr: int, rows: int, col
     return lib().colibri_moe_dequantize_mxfp4(codes_ptr, scales_ptr, rows, cols, dtype, out_ptr, hip_stream)
 
 
-def _on_device_of(t, fn):
-    """fn() with t's device current (the kernels run on the current one)."""
+def _stream_of(t, stream):
+    """Handle of `stream`, or of the current stream of t's device (its raw
+    handle: building a Stream object costs as much as the launch)."""
+    import torch
+
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _on_device_of(t, fn, *args):
+    """fn(*args) with t's device current (kernels run on the current one)."""
     import torch
 
     if t.device.index == torch.cuda.current_device():
-        return fn()
+        return fn(*args)
     with torch.cuda.device(t.device):
-        return fn()
+        return fn(*args)
 
 
 def quantize_mxfp4(w, stream=None):
@@ -201,9 +209,11 @@ def quantize_mxfp4(w, stream=None):
     scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=w.device)
     if rows == 0 or cols == 0:
         return codes, scales
-    st = _on_device_of(w, lambda: colibri_moe_quantize_mxfp4(
-        w.data_ptr(), BF16 if bf16 else F32, rows, cols, row_stride if rows > 1 else cols, codes.data_ptr(),
-        scales.data_ptr(), (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+    st = _on_device_of(w, colibri_moe_quantize_mxfp4, w.data_ptr(), BF16 if bf16 else F32, rows, cols,
+                       row_stride if rows > 1 else cols, codes.data_ptr(), scales.data_ptr(), _stream_of(w, stream))
+    if stream is not None:  # the tensors belong to the current stream, their memory waits for this one
+        for t in (w, codes, scales):
+            t.record_stream(stream)
     if st != OK:
         raise ColibriError("colibri_moe_quantize_mxfp4", st)
     return codes, scales
@@ -228,9 +238,11 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     out = torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32, device=codes.device)
     if rows == 0 or cols == 0:
         return out
-    st = _on_device_of(codes, lambda: colibri_moe_dequantize_mxfp4(
-        codes.data_ptr(), scales.data_ptr(), rows, cols, BF16 if bf16 else F32, out.data_ptr(),
-        (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+    st = _on_device_of(codes, colibri_moe_dequantize_mxfp4, codes.data_ptr(), scales.data_ptr(), rows, cols,
+                       BF16 if bf16 else F32, out.data_ptr(), _stream_of(codes, stream))
+    if stream is not None:
+        for t in (codes, scales, out):
+            t.record_stream(stream)
     if st != OK:
         raise ColibriError("colibri_moe_dequantize_mxfp4", st)
     return out
