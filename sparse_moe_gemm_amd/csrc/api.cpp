@@ -76,8 +76,8 @@ struct colibri_moe {
     Workspace ws; // in the arena, sized for max_tokens
     uint16_t* few_h;  // h of colibri_moe_forward_few [2][few tokens * k][f], bf16 layers
     int few_split;      // parts of its down kernel's sums,
-    float* few_part;    // their sums [d/32][few_split][512]
-    int32_t* few_count; // and arrivals per 32 columns [d/32], zero between calls
+    float* few_part;    // their sums [few_split][16][d]
+    int32_t* few_count; // and arrivals per column block (at most [d/32]), zero between calls
     int32_t* ccnt;  // fused combine: arrivals per token and 128-column tile [max_tokens][d/128], zero between calls
     bool timing;
     hipEvent_t ev[kStages + 1];
@@ -117,6 +117,24 @@ bool aligned16(const void* p)
 {
     return ((uintptr_t)p & 15u) == 0;
 }
+
+// Makes a device current for as long as it lives. The handle's kernels run on
+// the handle's device, whichever the calling thread works on (a NULL stream
+// means the current device's).
+struct OnDevice {
+    int before = -1;
+    explicit OnDevice(int device)
+    {
+        int now = -1;
+        if (hipGetDevice(&now) == hipSuccess && now != device && hipSetDevice(device) == hipSuccess)
+            before = now;
+    }
+    ~OnDevice()
+    {
+        if (before >= 0)
+            (void)hipSetDevice(before);
+    }
+};
 
 size_t round_up(size_t v, size_t a)
 {
@@ -304,9 +322,9 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     const size_t few_rows = (size_t)std::min(c.max_tokens, (int32_t)COLIBRI_MOE_FEW_TOKENS) * c.top_k;
     const bool few = c.dtype == COLIBRI_MOE_BF16;
     const size_t o_few = few ? cv.take(2 * few_rows * f * sizeof(uint16_t)) : 0;
-    h->few_split = few ? few_down_split((int)d, h->cus) : 1;
-    const size_t o_fpart = few ? cv.take(d / 32 * h->few_split * 512 * sizeof(float)) : 0;
-    const size_t o_fcount = few ? cv.take(d / 32 * sizeof(int32_t)) : 0;
+    h->few_split = few ? few_down_split((int)d, h->mx4, h->cus) : 1;
+    const size_t o_fpart = h->few_split > 1 ? cv.take(d * h->few_split * kFewTokens * sizeof(float)) : 0;
+    const size_t o_fcount = h->few_split > 1 ? cv.take(d / 32 * sizeof(int32_t)) : 0;
     const size_t o_ws = cv.take(layout_workspace(h, c.max_tokens, true, nullptr, nullptr));
     h->arena_bytes = cv.off;
 
@@ -326,14 +344,14 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     h->m_d = h->mx4 ? base + o_md : nullptr;
     h->ccnt = h->fuse_combine ? (int32_t*)(base + o_ccnt) : nullptr;
     h->few_h = few ? (uint16_t*)(base + o_few) : nullptr;
-    h->few_part = few ? (float*)(base + o_fpart) : nullptr;
-    h->few_count = few ? (int32_t*)(base + o_fcount) : nullptr;
+    h->few_part = h->few_split > 1 ? (float*)(base + o_fpart) : nullptr;
+    h->few_count = h->few_split > 1 ? (int32_t*)(base + o_fcount) : nullptr;
     layout_workspace(h, c.max_tokens, true, base + o_ws, &h->ws);
 
     hipStream_t s = h->stream;
     if (h->ccnt)
         CMOE_HIP(hipMemsetAsync(h->ccnt, 0, (size_t)c.max_tokens * (d / 128) * sizeof(int32_t), s));
-    if (few)
+    if (h->few_count)
         CMOE_HIP(hipMemsetAsync(h->few_count, 0, d / 32 * sizeof(int32_t), s));
     CMOE_HIP(launch_transpose_router(w->w_router, h->w_rt, (int)d, (int)E, (int)es, s));
     if (w->b_router)
@@ -490,6 +508,7 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
                                   const colibri_moe_routing_t& ro, const Workspace& ws, bool fused_ok)
 {
     const colibri_moe_config_t& c = h->cfg;
+    const OnDevice on(h->device);
     // Caller-provided routing buffers double as the working buffers (no copy).
     float* topw = ro.topk_w ? ro.topk_w : ws.topw;
     int32_t* ids = ro.topk_ids ? ro.topk_ids : ws.ids;
@@ -701,6 +720,7 @@ colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, in
         return COLIBRI_MOE_ERR_TOO_LARGE;
     if (skip)
         return COLIBRI_MOE_OK;
+    const OnDevice on(h->device);
     hipStream_t s = h->stream;
     const bool tm = h->timing;
     FewArgs a{};

@@ -282,11 +282,12 @@ struct FewArgs {
     uint16_t* h;           // [2][T*k][f] bf16: high and low parts
     void* y;               // [T][d] bf16
     int split;             // parts of the down kernel's sums (few_down_split)
-    float* part;           // split > 1: [d/32][split][512] their sums
-    int32_t* count;        // [d/32] parts finished, zero between calls
+    float* part;           // split > 1: [d/columns][split][16][columns] their sums
+    int32_t* count;        // [d/columns] parts finished, zero between calls
 };
 constexpr int kFewMaxSplit = 8;
-int few_down_split(int d, int cus);
+int few_down_columns(int mx4);            // columns of y per workgroup of the down kernel
+int few_down_split(int d, int mx4, int cus);
 // Whether the first launch computes the routing (else launch_router_bf16 runs
 // before it).
 bool few_routes_itself(int d, int E);

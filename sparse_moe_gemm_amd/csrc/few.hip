@@ -528,18 +528,27 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs g)
     }
 }
 
+// 16-row groups of W_down per item of the down kernel.
+__host__ __device__ constexpr int down_groups(int fmt)
+{
+    return fmt == kMx4 ? 4 : 2;
+}
+
 // Loads of B units of the down kernel: weights and scales of both 16-row
 // halves, and the token fragments of h (lanes whose token did not choose the
 // expert load nothing and hold zeros). H = 2: high and low parts apart, for 16
 // tokens; H = 1: at most 8 tokens, whose high parts are columns 0..7 and low
 // parts columns 8..15 of one fragment.
-template <int FMT, int B, int H>
+template <int FMT, int B, int H, int W>
 struct DownStep {
     static constexpr int M = Unit<FMT>::M;
-    Vec16 w[B][2];
-    uint32_t mx[FMT == kMx4 ? B : 1][2];
-    float sc[FMT == kFp8 ? B : 1][2];
-    Vec16 x[B][M][H];
+    static constexpr bool LATE = FMT == kMx4 && H == 2;  // (two sets of 16 fragments spill)
+    Vec16 w[B][W];
+    uint32_t mx[FMT == kMx4 ? B : 1][W];
+    float sc[FMT == kFp8 ? B : 1][W];
+    Vec16 x[LATE ? 1 : B][M][H];
+    uint32_t row[LATE ? B : 1];  // LATE: where x is, loaded just before it is multiplied
+    int at[LATE ? B : 1];
     float wt[B];  // routing weight, -1 if the lane's token did not choose the expert
 };
 
@@ -557,7 +566,8 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
     constexpr int M = U::M;
     constexpr int B = FMT == kBf16 ? (H == 1 ? 4 : 3) : FMT == kFp8 && H == 1 ? 2 : 1;
     __shared__ Routes r;
-    __shared__ __align__(16) float red[kWaves][512];
+    constexpr int W = down_groups(FMT), NC = 16 * W;  // 16-row groups, columns of an item
+    __shared__ __align__(16) float red[kWaves][W * 256];
     __shared__ int last;
 
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -577,17 +587,20 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
     const int nb = (int)blockIdx.x / g.split, part = (int)blockIdx.x - nb * g.split;
     const int v0 = (int)((int64_t)part * nact * NU / g.split);
     const int V = (int)((int64_t)(part + 1) * nact * NU / g.split);  // units v0 .. V of the item
-    floatx4 total[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    floatx4 total[W];
+#pragma unroll
+    for (int h = 0; h < W; ++h)
+        total[h] = floatx4{0.f, 0.f, 0.f, 0.f};
     // The wave's next unit to load: unit cu of active expert ca, of whose
     // tokens and weights cwt, crow, cw, cm, cs tell.
     int cv = v0 + wv, ca = -1, cu = 0;
-    float cwt = 0.f, cs[2] = {1.f, 1.f};
+    float cwt = 0.f, cs[2] = {1.f, 1.f};  // (8-bit weights: W = 2)
     uint32_t crow = 0;
     const uint8_t *cw = nullptr, *cm = nullptr;
     auto open = [&](int a) {
         ca = a;
         const int e = __builtin_amdgcn_readfirstlane(r.act[a]);
-        const int64_t rb = (int64_t)e * NBK + nb;
+        const int64_t rb = (int64_t)e * NBK + nb * (W / 2);
         const Choice ch = r.tab[a][H == 1 ? lane & 7 : lane & 15];
         cwt = ch.row < 0 ? -1.f : ch.w;
         // past the buffer for lanes that hold zeros
@@ -596,32 +609,42 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
             crow += plane;
         cw = uniform((const uint8_t*)g.w_d + rb * KB * 1024);
         if constexpr (FMT == kMx4)
-            cm = uniform(g.m_d + mx_scale_group(e, nb, 0, g.d, g.f) + mx_scale_at(nb, 0, 0));
+            cm = uniform(g.m_d + mx_scale_group(e, nb * (W / 2), 0, g.d, g.f) + mx_scale_at(nb * (W / 2), 0, 0));
         if constexpr (FMT == kFp8)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 cs[h] = ((const float*)uniform(g.s_d + rb * 32))[16 * h + (lane & 15)];
     };
-    auto load = [&](DownStep<FMT, B, H>& t) {
+    auto load_x = [&](Vec16 (&x)[M][H], uint32_t row, int at) {
+#pragma unroll
+        for (int s = 0; s < M; ++s)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                x[s][h] = __builtin_bit_cast(
+                    Vec16, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(row + 16u * s), at + h * (int)plane, 0));
+    };
+    constexpr bool LATE = DownStep<FMT, B, H, W>::LATE;
+    auto load = [&](DownStep<FMT, B, H, W>& t) {
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             t.wt[b] = cwt;
             const uint8_t* wp = cw + (int64_t)cu * 2048;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                t.w[b][h] = __builtin_nontemporal_load((const Vec16*)(wp + lane_w + h * 256));
+            for (int h = 0; h < W; ++h) {
+                t.w[b][h] = __builtin_nontemporal_load(
+                    (const Vec16*)(wp + (int64_t)(h / 2) * KB * 1024 + lane_w + h % 2 * 256));
                 if constexpr (FMT == kMx4)
-                    t.mx[b][h] = (cm + (int64_t)cu * 1024)[lane_m + h * 32];
+                    t.mx[b][h] = (cm + (int64_t)cu * 1024)[lane_m + h / 2 * 128 + h % 2 * 32];
                 if constexpr (FMT == kFp8)
                     t.sc[b][h] = cs[h];
             }
             const int at = cu * U::K * 2;
-#pragma unroll
-            for (int s = 0; s < M; ++s)
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-                    t.x[b][s][h] = __builtin_bit_cast(
-                        Vec16, __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(crow + 16u * s), at + h * (int)plane, 0));
+            if constexpr (LATE) {
+                t.row[b] = crow;
+                t.at[b] = at;
+            } else {
+                load_x(t.x[b], crow, at);
+            }
             if (cv + kWaves < V) {  // else this unit again, not multiplied
                 cv += kWaves;
                 cu += kWaves;
@@ -635,16 +658,19 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
             }
         }
     };
-    auto multiply = [&](const DownStep<FMT, B, H>& t, int i0) {
+    auto multiply = [&](const DownStep<FMT, B, H, W>& t, int i0) {
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             if (v0 + wv + kWaves * (i0 + b) >= V)
                 continue;
-            floatx4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            floatx4 acc[W];
+#pragma unroll
+            for (int h = 0; h < W; ++h)
+                acc[h] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < M; ++s)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < W; ++h) {
                     const float sc = FMT == kMx4 ? mx_scale(t.mx[FMT == kMx4 ? b : 0][h]) : t.sc[FMT == kFp8 ? b : 0][h];
                     const bf16x8 f = unit_frag<FMT>(t.w[b][h], s, sc);
 #pragma unroll
@@ -654,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
             // only the tokens that chose this expert take its rows (whose
             // weights may be infinite or NaN)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < W; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     total[h][i] = t.wt[b] < 0.f ? total[h][i] : fmaf(t.wt[b], acc[h][i], total[h][i]);
@@ -669,21 +695,25 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
             ++a;
         }
         open(a);
-        DownStep<FMT, B, H> t0, t1;
+        DownStep<FMT, B, H, W> t0, t1;
         load(t0);
         for (int i = 0; i < I; i += 2 * B) {
+            if constexpr (LATE)
+                load_x(t0.x[0], t0.row[0], t0.at[0]);  // before the next weights: the wait for it leaves them in flight
             load(t1);
             multiply(t0, i);
+            if constexpr (LATE)
+                load_x(t1.x[0], t1.row[0], t1.at[0]);
             load(t0);
             multiply(t1, i + B);
         }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < W; ++h)
         *(floatx4*)(&red[wv][h * 256 + lane * 4]) = total[h];
     lds_barrier();
     float sum = 0.f;
-    if (tid < 512)
+    if (tid < W * 256)
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
             sum += H == 1 ? red[w][tid] + red[w][tid ^ 32] : red[w][tid];  // ^ 32: eight columns on
@@ -692,8 +722,8 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
         // read past the XCDs' separate L2s), ordered by the wait for the stores
         // and the barrier before the count. Fences would do the same by
         // flushing every L2 from every wave, which took 115 us here.
-        float* mine = g.part + (int64_t)blockIdx.x * 512;
-        if (tid < 512)
+        float* mine = g.part + (int64_t)blockIdx.x * (W * 256);
+        if (tid < W * 256)
             __hip_atomic_store(mine + tid, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
@@ -706,11 +736,11 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
             __hip_atomic_store(&g.count[nb], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         float v[kFewMaxSplit];
         sum = 0.f;
-        if (tid < 512) {
+        if (tid < W * 256) {
 #pragma unroll
             for (int p = 0; p < kFewMaxSplit; ++p)
                 if (p < g.split)
-                    v[p] = __hip_atomic_load(g.part + ((int64_t)nb * g.split + p) * 512 + tid, __ATOMIC_RELAXED,
+                    v[p] = __hip_atomic_load(g.part + ((int64_t)nb * g.split + p) * (W * 256) + tid, __ATOMIC_RELAXED,
                                              __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
             for (int p = 0; p < kFewMaxSplit; ++p)
@@ -718,8 +748,8 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
                     sum += v[p];
         }
     }
-    if (tid < 512) {
-        const int el = tid % 256, t = (el / 4) % 16, col = nb * 32 + tid / 256 * 16 + 4 * (el / 64) + el % 4;
+    if (tid < W * 256) {
+        const int el = tid % 256, t = (el / 4) % 16, col = nb * NC + tid / 256 * 16 + 4 * (el / 64) + el % 4;
         if (t < g.T)
             ((uint16_t*)g.y)[(int64_t)t * g.d + col] = f32_to_bf16_bits(sum);
     }
@@ -744,16 +774,21 @@ hipError_t launch_few_gate_up(const FewArgs& a, int cus, hipStream_t s)
     return hipGetLastError();
 }
 
-int few_down_split(int d, int cus)
+int few_down_columns(int mx4)
+{
+    return 16 * down_groups(mx4 ? kMx4 : kBf16);
+}
+
+int few_down_split(int d, int mx4, int cus)
 {
     // A workgroup per compute unit, in at most kFewMaxSplit parts: reading the
     // weights at full rate takes them all.
-    return std::max(1, std::min(kFewMaxSplit, cus / (d / 32)));
+    return std::max(1, std::min(kFewMaxSplit, cus / (d / few_down_columns(mx4))));
 }
 
 hipError_t launch_few_down(const FewArgs& a, hipStream_t s)
 {
-    const dim3 grid(a.d / 32 * a.split), block(kThreads);
+    const dim3 grid(a.d / few_down_columns(a.m_gu != nullptr) * a.split), block(kThreads);
     auto k = a.m_gu   ? (a.T <= 8 ? few_down_kernel<kMx4, 1> : few_down_kernel<kMx4, 2>)
              : a.s_gu ? (a.T <= 8 ? few_down_kernel<kFp8, 1> : few_down_kernel<kFp8, 2>)
                       : (a.T <= 8 ? few_down_kernel<kBf16, 1> : few_down_kernel<kBf16, 2>);
