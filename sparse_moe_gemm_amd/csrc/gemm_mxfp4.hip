@@ -343,20 +343,21 @@ hipError_t launch_shape(const MxGemmArgs& a, hipStream_t s)
 // Rows per tile from the mean rows per expert (the routing is on the device).
 // A tile costs its weights' stages whatever rows it holds, and its multiplied
 // row groups; an expert with a few rows more than the tile pays for two.
-// Measured (gate/up GEMM, us, tiles of 32 / 64 / 128 / 256 rows), bf16 rows:
-// 8 experts of 4096 x 14336 with 8 rows on average 97 / 98 / 105 / 139, 32 rows
-// 140 / 112 / 115 / 154, 83 rows 220 / 178 / 164 / 201, 1024 rows 2044 / 1595 /
-// 1496 / 1478; 128 of 2048 x 768 with 10 rows 44 / 44 / 46 / 59, 64 rows 96 / 73 /
-// 67 / 83. 4-bit rows: 8 rows 93 / 94 / 96 / 94, 250 rows 551 / 317 / 219 / 230,
-// 1024 rows 1356 / 951 / 713 / 671.
+// Gate/up GEMM in us with tiles of 32 / 64 / 128 / 256 rows, bf16 rows: 8 experts
+// of 4096 x 14336 with 8 rows on average 97 / 98 / 105 / 139, 32 rows 140 / 112 /
+// 115 / 154, 83 rows 220 / 178 / 164 / 201, 1024 rows 2044 / 1595 / 1496 / 1478
+// (down 974 / 819 / 803 / 834); 128 of 2048 x 768 with 10 rows 44 / 44 / 46 / 59,
+// 64 rows 96 / 73 / 67 / 83. 4-bit rows (64 / 128 / 256): 8 x 4096 x 14336 with
+// 8 rows 92 / 92 / 92, 83 rows 145 / 111 / 113, 175 rows 222 / 161 / 143, 1024
+// rows 735 / 586 / 571; 128 x 2048 x 768 with 128 rows 91 / 71 / 61; 64 x 4096 x
+// 1408 with two experts taking most rows, mean 10: 45 / 46 / 54, mean 31: 86 /
+// 79 / 81, mean 128: 143 / 133 / 142.
 int mx_tile_rows(int A, int E, bool a4)
 {
     const int64_t mean = ((int64_t)A + E - 1) / E;
-    if (mean <= 20 && !a4)
-        return 32;
-    if (mean <= 40)
-        return 64;
-    return mean >= 400 && a4 ? 256 : 128;
+    if (a4)
+        return mean <= 20 ? 64 : mean <= 100 ? 128 : 256;
+    return mean <= 20 ? 32 : mean <= 40 ? 64 : 128;
 }
 
 }  // namespace
