@@ -12,7 +12,9 @@
 //             v_mfma_scale_f32_32x32x64_f8f6f4, 4-bit codes on both sides, one
 //             scale byte per lane: products of 4-bit values are multiples of
 //             1/4 up to 36, whose sums within a block are exact.
-// Both sum in fp32.
+// Both sum in fp32. H is stored as bf16 (the activation type and the down
+// GEMM's MFMA operand, relative error 2^-8), expert outputs stay fp32 until the
+// combine.
 //
 // A tile is BM sorted rows of one expert x 256 weight rows (x a K split); a
 // persistent workgroup walks its tiles (tiles.hpp) and streams their K stages
@@ -20,11 +22,22 @@
 // while stage s is multiplied, the next SLOTS - 1 are on their way, across tile
 // borders too. One wait and one barrier per stage: after it every wave's loads
 // of stage s are in LDS and every wave has read stage s - 1 to the end, so its
-// slot can take stage s + SLOTS - 1.
+// slot can take stage s + SLOTS - 1. Weights are streamed straight into LDS in
+// whole 1 KiB blocks, which keeps enough of them in flight to read HBM at 5.1 -
+// 5.4 TB/s from experts of a few rows (32 tokens on 8 experts of 4096 x 14336:
+// gate/up 499 MB in 92 us, down 249 MB in 48 us; streaming them into registers
+// without LDS took 133 and 88 us).
 // Waves form WAVES_M x 4; a wave multiplies WM = BM / WAVES_M rows with 64
 // weight rows (one gate and one up block of 32, so SiLU(g)*u stays in its
 // registers). The weight fragment is the MFMA's first operand: a result lane
 // holds one token row and groups of four consecutive outputs.
+//
+// With many rows (8 experts, 4096 tokens, k = 2): down 0.96 TFLOP in 790 - 840 us
+// (1.15 - 1.2 PFLOP/s, 58% MFMA busy at 1.84 GHz; random bf16 operands alone, no
+// loads, run at 1.6 PFLOP/s under the power limit); gate/up on 4-bit rows 1.92
+// TFLOP in 510 - 530 us (3.7 PFLOP/s; alone 6.3), bound by what the stages move:
+// 35 KB into LDS and 96 KB out of it for 1024 MFMA cycles. A wave tile of 128 x
+// 128 would read a third less but spills.
 #include "lds_dma.hpp"
 #include "mxfp4.hpp"
 #include "tiles.hpp"
@@ -45,6 +58,13 @@ __device__ __forceinline__ float silu_fast(float z)
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b)
 {
     return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+
+// fn(0), fn(1), ... with the numbers as types.
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F fn)
+{
+    (fn(std::integral_constant<int, I>{}), ...);
 }
 
 // One K stage: the token rows (64 k of BM bf16 rows, 128 bytes each; or 128 k of
@@ -154,32 +174,40 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
         c.left = t.nkt;
         c.L = L;
     };
-    // Requests the cursor's stage into slot `slot` and moves the cursor on;
-    // past the last tile it requests the last stage again (read by no one),
-    // which keeps the loads in flight per stage the same.
-    auto request = [&](MxCursor<Sh::A_INS>& c, int slot) {
-        const uint32_t base = ring0 + (uint32_t)slot * (uint32_t)sizeof(Stage);
-#pragma unroll
-        for (int q = 0; q < Sh::A_INS; ++q) {
+    // Load q (of NLD) of this wave's share of the cursor's stage into the slot
+    // at LDS address base.
+    auto piece = [&](const MxCursor<Sh::A_INS>& c, uint32_t base, auto q_const) {
+        constexpr int q = decltype(q_const)::value;
+        if constexpr (q < Sh::A_INS) {
             const int i = (wv * Sh::A_INS + q) % Sh::A_ALL;
             const uint32_t to = base + (uint32_t)offsetof(Stage, a) + (uint32_t)i * 1024u;
             if constexpr (A4)
                 lds_load16(c.ra, lane16, ((uint32_t)(i / 2) * (uint32_t)KB + (uint32_t)(c.kt * 2 + i % 2)) * 1024u, to);
             else
                 lds_load16(ra, c.aoff[q], (uint32_t)c.kt * 128u, to);
-        }
-#pragma unroll
-        for (int q = 0; q < Sh::B_INS; ++q) {
-            const int i = wv * Sh::B_INS + q;  // row block i / KBS, k block i % KBS of the stage
+        } else if constexpr (q < Sh::A_INS + Sh::B_INS) {
+            const int i = wv * Sh::B_INS + q - Sh::A_INS;  // row block i / KBS, k block i % KBS of the stage
             lds_load16(c.rb, lane16,
                        ((uint32_t)(i / Stage::KBS) * (uint32_t)KB + (uint32_t)(c.kt * Stage::KBS + i % Stage::KBS)) * 1024u,
                        base + (uint32_t)offsetof(Stage, b) + (uint32_t)i * 1024u);
-        }
-        lds_load4(c.rs, lane4, (uint32_t)(c.kt * Stage::KBS / 2) * 1024u + (uint32_t)(wv % 4) * 256u,
-                  base + (uint32_t)offsetof(Stage, bs) + (uint32_t)(wv % 4) * 256u);
-        if constexpr (A4)
+        } else if constexpr (q == Sh::A_INS + Sh::B_INS) {
+            lds_load4(c.rs, lane4, (uint32_t)(c.kt * Stage::KBS / 2) * 1024u + (uint32_t)(wv % 4) * 256u,
+                      base + (uint32_t)offsetof(Stage, bs) + (uint32_t)(wv % 4) * 256u);
+        } else {
             lds_load4(c.ras, lane4 + (uint32_t)(wv % Sh::AS_ALL) * 256u, (uint32_t)c.kt * (uint32_t)MB * 128u,
                       base + (uint32_t)offsetof(Stage, as) + (uint32_t)(wv % Sh::AS_ALL) * 256u);
+        }
+    };
+    // Pieces Q0 .. Q1 of a stage.
+    auto pieces = [&](const MxCursor<Sh::A_INS>& c, uint32_t base, auto q0_const, auto q1_const) {
+        constexpr int Q0 = decltype(q0_const)::value, Q1 = decltype(q1_const)::value;
+        each(std::make_integer_sequence<int, Q1 - Q0>{},
+             [&](auto i) { piece(c, base, std::integral_constant<int, Q0 + decltype(i)::value>{}); });
+    };
+    // The cursor moves on; past the last tile it stays, and the last stage is
+    // loaded again (read by no one), which keeps the loads in flight per stage
+    // the same.
+    auto advance = [&](MxCursor<Sh::A_INS>& c) {
         if (c.left > 1) {
             ++c.kt;
             --c.left;
@@ -187,12 +215,15 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
             open(c, c.L + GRID);
         }
     };
+    auto slot_at = [&](int slot) { return ring0 + (uint32_t)slot * (uint32_t)sizeof(Stage); };
 
     MxCursor<Sh::A_INS> cur;
     open(cur, blockIdx.x);
 #pragma unroll
-    for (int q = 0; q < SLOTS - 1; ++q)
-        request(cur, q);
+    for (int q = 0; q < SLOTS - 1; ++q) {
+        pieces(cur, slot_at(q), std::integral_constant<int, 0>{}, std::integral_constant<int, Sh::NLD>{});
+        advance(cur);
+    }
     int slot = 0;
 
     for (int L = blockIdx.x; L < total; L += GRID) {
@@ -211,75 +242,115 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_pe
         // All K stages with the first RGC row groups multiplied.
         auto stages = [&](auto rg_const) {
             constexpr int RGC = decltype(rg_const)::value;
-            for (int j = 0; j < t.nkt; ++j) {
-                // (LDS reads too: the compiler may move the MFMAs that use them
-                // past the barrier, and their waits with them)
+            auto stage = [&](int j) {
+                // Its own loads of the stage have landed, and its LDS reads of the
+                // one before (the compiler may move the MFMAs that use them past
+                // the barrier, and their waits with them, while the slot they
+                // read is filled anew behind it).
                 wait_vm<Sh::NLD * (SLOTS - 2)>();
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                request(cur, slot == 0 ? SLOTS - 1 : slot - 1);
+                const uint32_t fill = slot_at(slot == 0 ? SLOTS - 1 : slot - 1);
                 const Stage& st = ring[slot];
                 const int kb = (t.kt0 + j) * Stage::KBS;
-                if constexpr (RGC > 0) {
-                    if constexpr (A4) {
-                        uint32_t sb[2], sa[RGC];
+                if constexpr (RGC == 0 || !A4)
+                    pieces(cur, fill, std::integral_constant<int, 0>{}, std::integral_constant<int, Sh::NLD>{});
+                if constexpr (RGC > 0 && A4) {
+                    uint32_t sb[2], sa[RGC];
+                    Vec16 wb[2][2], wa[2][RGC];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
-                            sb[n] = st.bs[(wn * 2 + n) * kWave + lane];
+                            wb[s][n] = st.b[((wn * 2 + n) * 2 + s) * kWave + lane];
+                        if (s == 0) {
 #pragma unroll
-                        for (int i = 0; i < RGC; ++i)
-                            sa[i] = st.as[(wm * MI + i) * kWave + lane];
-                        auto step = [&](auto s_const) {
-                            constexpr int s = decltype(s_const)::value;
-                            v8i fb[2], fa[RGC];
-#pragma unroll
-                            for (int n = 0; n < 2; ++n) {
-                                const Vec16 w = st.b[((wn * 2 + n) * 2 + s) * kWave + lane];
-                                fb[n] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-                            }
-#pragma unroll
-                            for (int i = 0; i < RGC; ++i) {
-                                const Vec16 w = st.a[((wm * MI + i) * 2 + s) * kWave + lane];
-                                fa[i] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-                            }
+                            for (int n = 0; n < 2; ++n)
+                                sb[n] = st.bs[(wn * 2 + n) * kWave + lane];
 #pragma unroll
                             for (int i = 0; i < RGC; ++i)
+                                sa[i] = st.as[(wm * MI + i) * kWave + lane];
+                        }
+#pragma unroll
+                        for (int i = 0; i < RGC; ++i)
+                            wa[s][i] = st.a[((wm * MI + i) * 2 + s) * kWave + lane];
+                    }
+                    auto step = [&](auto s_const) {
+                        constexpr int s = decltype(s_const)::value;
+                        auto wide = [](const Vec16& w) {
+                            return v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                        };
+                        auto row = [&](auto i_const) {
+                            constexpr int i = decltype(i_const)::value;
+                            if constexpr (i < RGC) {
+                                // The next loads are spread over the MFMAs, in the order
+                                // written: all issued first they hold every wave up at the
+                                // load unit (8 x 14336, 4096 tokens: 590 -> 520 us; reading
+                                // the fragments half a stage ahead as well gained nothing).
+                                constexpr int m = s * RGC + i;
+                                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                                 for (int n = 0; n < 2; ++n)
                                     acc[n][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                        fb[n], fa[i], acc[n][i], 4, 4, s, (int)sb[n], s, (int)sa[i]);
+                                        wide(wb[s][n]), wide(wa[s][i]), acc[n][i], 4, 4, s, (int)sb[n], s, (int)sa[i]);
+                                __builtin_amdgcn_sched_barrier(0);
+                                pieces(cur, fill, std::integral_constant<int, m * Sh::NLD / (2 * RGC)>{},
+                                       std::integral_constant<int, (m + 1) * Sh::NLD / (2 * RGC)>{});
+                            }
                         };
-                        step(std::integral_constant<int, 0>{});
-                        step(std::integral_constant<int, 1>{});
-                    } else {
-                        Vec16 wb[2];
-                        float sc[2];
+                        row(std::integral_constant<int, 0>{});
+                        row(std::integral_constant<int, 1>{});
+                        row(std::integral_constant<int, 2>{});
+                        row(std::integral_constant<int, 3>{});
+                    };
+                    step(std::integral_constant<int, 0>{});
+                    step(std::integral_constant<int, 1>{});
+                    __builtin_amdgcn_sched_barrier(0);
+                } else if constexpr (RGC > 0) {
+                    Vec16 wb[2];
+                    float sc[2];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            wb[n] = st.b[(wn * 2 + n) * kWave + lane];
-                            sc[n] = mx_scale(((const uint8_t*)st.bs)[((wn * 2 + n) * kWave + lane) * 2 + (kb & 1)]);
+                    for (int n = 0; n < 2; ++n) {
+                        wb[n] = st.b[(wn * 2 + n) * kWave + lane];
+                        sc[n] = mx_scale(((const uint8_t*)st.bs)[((wn * 2 + n) * kWave + lane) * 2 + (kb & 1)]);
+                    }
+                    auto step = [&](auto s_const) {
+                        constexpr int s = decltype(s_const)::value;
+                        bf16x8 fb[2], fa[RGC];
+#pragma unroll
+                        for (int i = 0; i < RGC; ++i) {
+                            const int r = wm * Sh::WM + i * 32 + (lane & 31);
+                            fa[i] = as_bf16x8(st.a[r * 8 + mx_swz(r, 4 * half + s)]);
                         }
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            bf16x8 fb[2], fa[RGC];
+                        for (int n = 0; n < 2; ++n)
+                            fb[n] = mx8_to_bf16(wb[n][s], sc[n]);
 #pragma unroll
-                            for (int i = 0; i < RGC; ++i) {
-                                const int r = wm * Sh::WM + i * 32 + (lane & 31);
-                                fa[i] = as_bf16x8(st.a[r * 8 + mx_swz(r, 4 * half + s)]);
-                            }
+                        for (int i = 0; i < RGC; ++i)
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
-                                fb[n] = mx8_to_bf16(wb[n][s], sc[n]);
-#pragma unroll
-                            for (int i = 0; i < RGC; ++i)
-#pragma unroll
-                                for (int n = 0; n < 2; ++n)
-                                    acc[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[i], acc[n][i], 0, 0, 0);
-                        }
-                    }
+                                acc[n][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[i], acc[n][i], 0, 0, 0);
+                    };
+                    step(std::integral_constant<int, 0>{});
+                    step(std::integral_constant<int, 1>{});
+                    step(std::integral_constant<int, 2>{});
+                    step(std::integral_constant<int, 3>{});
                 }
                 slot = slot == SLOTS - 1 ? 0 : slot + 1;
+            };
+            // The cursor is SLOTS - 1 stages ahead: in this tile until the last
+            // SLOTS stages (a loop without branches: behind one the compiler sinks
+            // the MFMAs), then in the next.
+            int j = 0;
+            for (; j + SLOTS < t.nkt; ++j) {
+                stage(j);
+                ++cur.kt;
+                --cur.left;
+            }
+            for (; j < t.nkt; ++j) {
+                stage(j);
+                advance(cur);
             }
         };
         if (RG == MI)

@@ -27,19 +27,20 @@ __device__ __forceinline__ uint32_t lds_address(const void* p)
 // 64 lanes x 16 (lds_load16) or 4 bytes (lds_load4) from rsrc + voff + soff to
 // the 1 KiB (256 bytes) of LDS at byte address lds, lane l's piece at place l.
 // Inline assembly, so that the compiler adds no waits of its own before LDS
-// reads: whoever reads the data waits on vmcnt and a barrier first.
+// reads: whoever reads the data waits on vmcnt and a barrier first, with a
+// memory clobber there (none here: LDS reads of other places may pass).
 __device__ __forceinline__ void lds_load16(Rsrc rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
                  "s"(soff), "s"(lds)
-                 : "memory", "m0");
+                 : "m0");
 }
 
 __device__ __forceinline__ void lds_load4(Rsrc rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
                  "s"(soff), "s"(lds)
-                 : "memory", "m0");
+                 : "m0");
 }
 
 // Waits until at most N of this wave's vector memory operations (loads into
