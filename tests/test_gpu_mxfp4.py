@@ -14,7 +14,7 @@ import pytest
 
 import mx_ref
 import synth
-from moe_case import make_layer, run_gpu, to_dev
+from moe_case import make_layer, run_gpu, to_dev, to_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -176,9 +176,6 @@ def test_quantize_on_another_stream_and_in_a_graph():
 # --- layers --------------------------------------------------------------------
 
 
-PATHS = {"tiled": {"CMOE_DECODE_MAX_A": "0"},
-         "small-batch": {"CMOE_DECODE_MAX_A": "65536", "CMOE_DECODE_MAX_ROWS": "0"},
-         "default": {}}
 CASES = [
     C("decode-small", 32, 512, 8, 2, 1024, "bf16"),
     C("one-token", 1, 128, 8, 2, 128, "bf16"),
@@ -212,11 +209,8 @@ def reference(cfg, inp, act4):
 
 @pytest.mark.parametrize("act4", [False, True], ids=["w4a16", "w4a4"])
 @pytest.mark.parametrize("cfg", CASES, ids=[c.name for c in CASES])
-@pytest.mark.parametrize("path", list(PATHS))
-def test_mxfp4_layer(path, cfg, act4, monkeypatch):
-    for key, val in PATHS[path].items():
-        monkeypatch.setenv(key, val)
-    print(f"mxfp4 case {cfg} path {path} act4 {act4}", flush=True)
+def test_mxfp4_layer(cfg, act4):
+    print(f"mxfp4 case {cfg} act4 {act4}", flush=True)
     inp = synth.make_inputs(cfg)
     layer = make_layer(cfg, inp, flags=mx_flags(act4))
     g = run_gpu(layer, inp["x"])
@@ -251,25 +245,79 @@ def test_mxfp4_layer_from_values_read_back():
 
 
 @pytest.mark.parametrize("act4", [False, True], ids=["w4a16", "w4a4"])
-def test_mxfp4_device_choice_matches_each_path(act4, monkeypatch):
-    """Calls that enqueue both GEMM paths give the chosen path's results bit for
-    bit, and colibri_moe_forward_static the same as forward."""
-    for cfg in (C("few-rows", 200, 256, 64, 2, 256, "bf16"), C("many-rows", 200, 256, 4, 2, 256, "bf16")):
-        inp = synth.make_inputs(cfg)
-        got = {}
-        for path, env in PATHS.items():
-            with monkeypatch.context() as m:
-                for key, val in env.items():
-                    m.setenv(key, val)
-                layer = make_layer(cfg, inp, flags=mx_flags(act4))
-            got[path] = run_gpu(layer, inp["x"])
-            if path == "default":
-                ys = layer.forward(to_dev(inp["x"]), static_scratch=True)
-                assert np.array_equal(ys.double().cpu().numpy(), got[path]["y"])
-            layer.close()
-        rows = got["default"]["expert_counts"].max()
-        same = "small-batch" if rows <= 32 else "tiled"
-        assert np.array_equal(got["default"]["y"], got[same]["y"]), (cfg.name, rows)
+def test_mxfp4_static_scratch_and_every_token_count(act4):
+    """colibri_moe_forward_static gives forward's y bit for bit, for calls of
+    one token to all of them on one handle (every tile height of the rules),
+    and leaves the rows of y behind a call's tokens as they were."""
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    cfg = C("counts", 900, 256, 8, 2, 384, "bf16")
+    inp = synth.make_inputs(cfg)
+    layer = make_layer(cfg, inp, flags=mx_flags(act4))
+    x = to_dev(inp["x"])
+    ref = reference(cfg, inp, act4)
+    for T in (1, 2, 31, 33, 80, 81, 161, 400, 401, 900):
+        y = torch.full_like(x, 7.0)
+        rt = layer.routing_buffers(T)
+        assert cm.colibri_moe_forward(layer.handle, x.data_ptr(), T, y.data_ptr()) == cm.OK
+        ys = layer.forward(x[:T], routing=rt, static_scratch=True)
+        torch.cuda.synchronize()
+        assert torch.equal(ys, y[:T]) and bool(torch.all(y[T:] == 7.0)), T
+        g = dict(y=to_f64(ys), **{n: rt[n].cpu().numpy() for n in ("topk_ids", "topk_w")})
+        mx_ref.check_layer(g, tuple(v[:T] for v in ref), f"T={T}")
+    layer.close()
+
+
+@pytest.mark.parametrize("act4", [False, True], ids=["w4a16", "w4a4"])
+def test_from_a_quantized_checkpoint_to_single_tokens(act4):
+    """The operators as they are used together: expert weights arrive as codes
+    and scales, are read back and given to init; a prompt goes through forward,
+    and each next token (made from the last y) through forward_few, on the same
+    handle and without waiting. Every step is held against the 64-bit layer on
+    the codes' values and, for the same tokens, forward_few against forward."""
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    cfg = C("together", 75, 384, 16, 3, 256, "bf16")
+    inp = synth.make_inputs(cfg)
+    w64 = mx_ref.layer_weights(inp, mx_ref.rounded)
+    packed = {n: cm.quantize_mxfp4(to_dev(inp[n]).view(-1, inp[n].shape[-1])) for n in ("w_gate", "w_up", "w_down")}
+    wts = [cm.dequantize_mxfp4(*packed[n]).view(inp[n].shape) for n in packed]
+    for n, t in zip(("gate", "up", "down"), wts):
+        assert np.array_equal(to_f64(t), w64[n])  # exact in bf16
+    layer = cm.MoELayer(to_dev(inp["w_router"]), to_dev(inp["b_router"]), *wts, cfg.k, max_tokens=cfg.T,
+                        flags=cm.FLAG_ASYNC | mx_flags(act4))
+    del wts
+
+    def check(x, y, rt, h_eps, what):
+        x = to_f64(x)
+        ref = mx_ref.layer64(x, mx_ref.rounded(x) if act4 else x, w64, cfg.k, h_eps)
+        g = dict(y=to_f64(y), **{n: rt[n].cpu().numpy() for n in ("topk_ids", "topk_w")})
+        mx_ref.check_layer(g, ref, what)
+        return ref[1]
+
+    x = to_dev(inp["x"])
+    steps = []
+    rt = layer.routing_buffers(cfg.T)
+    y = layer.forward(x, routing=rt)
+    check(x, y, rt, 2.0 ** -8, "prompt")
+    for i, T in enumerate((1, 4, 1, 16, 1)):
+        xi = (x[-T:] * 0.5 + y[-T:]).contiguous()
+        rt, rt2 = layer.routing_buffers(T), layer.routing_buffers(T)
+        yi = layer.forward_few(xi, routing=rt)
+        y2 = layer.forward(xi, routing=rt2)
+        steps.append((xi, yi, rt, y2, rt2))
+        y = torch.cat([y, yi])
+    torch.cuda.synchronize()
+    for i, (xi, yi, rt, y2, rt2) in enumerate(steps):
+        assert torch.equal(rt["topk_ids"], rt2["topk_ids"]) and torch.equal(rt["topk_w"], rt2["topk_w"])
+        a = check(xi, yi, rt, 2.0 ** -16, f"step {i} few")
+        b = check(xi, y2, rt2, 2.0 ** -8, f"step {i} forward")
+        assert np.all(np.linalg.norm(to_f64(yi) - to_f64(y2), axis=1) <= a + b)
+    layer.close()
 
 
 @pytest.mark.parametrize("act4", [False, True], ids=["w4a16", "w4a4"])
