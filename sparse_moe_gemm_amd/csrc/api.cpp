@@ -34,7 +34,7 @@ const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_u
 
 // Per-call working memory of a forward, for A = T*k assignments: routing
 // buffers the caller did not supply, H, the fp32 partial sums, and the 8-bit
-// token rows of the W8A8 mode.
+// or 4-bit token rows of the modes that quantize them.
 struct Workspace {
     uint8_t* xq;  // q8: token rows as E4M3 codes [T][d]; q4: 4-bit rows by sorted position (mxfp4.hpp)
     float* xsc;   // q8: their scales by sorted position [A]
@@ -63,8 +63,8 @@ struct colibri_moe {
     void* w_rt;   // router weights in the router kernels' layout
     float* b_r;   // [E]
     void* w_gu;   // [E][2f][d], gate/up interleaved by 32 rows (bf16: blocked MFMA layout;
-                  // fp8: E4M3 codes in the fp8 blocked layout)
-    void* w_d;    // [E][d][f] (bf16: blocked MFMA layout; fp8: as w_gu)
+                  // fp8: E4M3 codes in the fp8 blocked layout; mx4: 4-bit codes, mxfp4.hpp)
+    void* w_d;    // [E][d][f] (bf16: blocked MFMA layout; fp8, mx4: as w_gu)
     float* s_gu;  // fp8 row scales [E][2f] (interleaved rows), else null
     float* s_d;   // fp8 row scales [E][d], else null
     uint8_t* m_gu;  // mx4: scale bytes of w_gu and w_d in the 4-bit GEMM layout

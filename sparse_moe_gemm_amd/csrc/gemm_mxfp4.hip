@@ -32,10 +32,10 @@
 // registers). The weight fragment is the MFMA's first operand: a result lane
 // holds one token row and groups of four consecutive outputs.
 //
-// With many rows (8 experts, 4096 tokens, k = 2): down 0.96 TFLOP in 790 - 840 us
-// (1.15 - 1.2 PFLOP/s, 58% MFMA busy at 1.84 GHz; random bf16 operands alone, no
+// With many rows (8 experts, 4096 tokens, k = 2): down 0.96 TFLOP in 770 - 840 us
+// (1.15 - 1.25 PFLOP/s, 61% MFMA busy at 1.86 GHz; random bf16 operands alone, no
 // loads, run at 1.6 PFLOP/s under the power limit); gate/up on 4-bit rows 1.92
-// TFLOP in 510 - 530 us (3.7 PFLOP/s; alone 6.3), bound by what the stages move:
+// TFLOP in 485 - 550 us (3.5 - 3.9 PFLOP/s; alone 6.3), bound by what the stages move:
 // 35 KB into LDS and 96 KB out of it for 1024 MFMA cycles. A wave tile of 128 x
 // 128 would read a third less but spills.
 #include "lds_dma.hpp"
