@@ -246,6 +246,29 @@ def test_few_on_two_streams_and_beside_forward():
         h[0].close()
 
 
+@pytest.mark.parametrize("E", [24, 200])
+def test_few_writes_only_the_routing_outputs_asked_for(E):
+    """Each routing output alone, and each left out, as in a call that asks for
+    all of them."""
+    import torch
+
+    cfg = C("partial", 9, 256, E, 3, 256, "bf16")
+    inp = synth.make_inputs(cfg)
+    layer = make_layer(cfg, inp)
+    x = to_dev(inp["x"])
+    full = layer.routing_buffers(9)
+    want = layer.forward_few(x, routing=full)
+    for name in full:
+        for keys in ([name], [n for n in full if n != name]):
+            rt = {n: torch.full_like(full[n], -5) for n in keys}
+            y = layer.forward_few(x, routing=rt)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), keys
+            for n in keys:
+                assert torch.equal(rt[n], full[n]), (n, keys)
+    layer.close()
+
+
 def test_few_stage_times():
     import sparse_moe_gemm_amd as cm
 
