@@ -25,7 +25,7 @@
 // slot can take stage s + SLOTS - 1. Weights are streamed straight into LDS in
 // whole 1 KiB blocks, which keeps enough of them in flight to read HBM at 5.1 -
 // 5.4 TB/s from experts of a few rows (32 tokens on 8 experts of 4096 x 14336:
-// gate/up 499 MB in 92 us, down 249 MB in 48 us; streaming them into registers
+// gate/up 499 MB in 90 us, down 249 MB in 47 us; streaming them into registers
 // without LDS took 133 and 88 us).
 // Waves form WAVES_M x 4; a wave multiplies WM = BM / WAVES_M rows with 64
 // weight rows (one gate and one up block of 32, so SiLU(g)*u stays in its
@@ -112,9 +112,24 @@ struct MxCursor {
     int L;                 // the tile's launch index
 };
 
+// Workgroups on a compute unit: what its LDS and registers hold, since their
+// barriers and loads then fall into each other's MFMAs. Three of four waves for
+// bf16 rows in tiles of 32 and 64 (53 KB each), against two with one more slot
+// each (67 and 70 KB), gate/up + down in us: 8 experts of 4096 x 14336 with 4
+// rows on average 99 + 53 -> 96 + 52, 32 rows 128 + 65 -> 110 + 62; 128 of 2048 x
+// 768 with 31 rows 53 + 38 -> 52 + 36; 64 of 4096 x 1408 with 31 rows 96 + 53 -> 91 +
+// 53, most of them on two experts 106 + 69 -> 111 + 63. (Four of three slots for
+// tiles of 32 rows: the same as three.)
+template <int BM, int WAVES_M, bool A4>
+__host__ __device__ constexpr int mx_groups()
+{
+    return WAVES_M > 1 ? 1 : BM <= 64 && !A4 ? 3 : 2;
+}
+
 template <int BM, int WAVES_M, int SLOTS, bool A4, bool GATE_UP>
-__global__ __launch_bounds__(WAVES_M * 4 * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx_gemm_kernel(
-    MxGemmArgs g)
+__global__ __launch_bounds__(WAVES_M * 4 * kWave)
+    __attribute__((amdgpu_waves_per_eu(WAVES_M * mx_groups<BM, WAVES_M, A4>(),
+                                       WAVES_M * mx_groups<BM, WAVES_M, A4>()))) void mx_gemm_kernel(MxGemmArgs g)
 {
     using Sh = MxShape<BM, WAVES_M, A4>;
     using Stage = typename Sh::Stage;
@@ -405,7 +420,7 @@ hipError_t launch_shape(const MxGemmArgs& a, hipStream_t s)
 {
     const int NT = ((GATE_UP ? 2 * a.f : a.d) + kBN - 1) / kBN;
     const int64_t tiles = ((int64_t)a.A_max / BM + a.E) * NT * (GATE_UP ? 1 : a.split);  // at most
-    const int grid = (int)std::min<int64_t>(tiles, WAVES_M == 1 ? 2 * a.cus : a.cus);
+    const int grid = (int)std::min<int64_t>(tiles, mx_groups<BM, WAVES_M, A4>() * a.cus);
     hipLaunchKernelGGL((mx_gemm_kernel<BM, WAVES_M, SLOTS, A4, GATE_UP>), dim3(grid), dim3(WAVES_M * 4 * kWave), 0, s,
                        a);
     return hipGetLastError();
@@ -414,11 +429,14 @@ hipError_t launch_shape(const MxGemmArgs& a, hipStream_t s)
 // Rows per tile from the mean rows per expert (the routing is on the device).
 // A tile costs its weights' stages whatever rows it holds, and its multiplied
 // row groups; an expert with a few rows more than the tile pays for two.
-// Gate/up GEMM in us with tiles of 32 / 64 / 128 / 256 rows, bf16 rows: 8 experts
-// of 4096 x 14336 with 8 rows on average 97 / 98 / 105 / 139, 32 rows 140 / 112 /
-// 115 / 154, 83 rows 220 / 178 / 164 / 201, 1024 rows 2044 / 1595 / 1496 / 1478
-// (down 974 / 819 / 803 / 834); 128 of 2048 x 768 with 10 rows 44 / 44 / 46 / 59,
-// 64 rows 96 / 73 / 67 / 83. 4-bit rows (64 / 128 / 256): 8 x 4096 x 14336 with
+// Gate/up + down in us with tiles of 64 / 128 rows, bf16 rows: 8 experts of
+// 4096 x 14336 with 45 rows on average 126 + 74 / 143 + 70, 64 rows 158 + 90 / 166 +
+// 102, 98 rows 201 + 111 / 207 + 103; 128 of 2048 x 768 with 44 rows 60 + 44 / 66 +
+// 47, 64 rows 95 + 56 / 73 + 53; 64 of 4096 x 1408 with 47 rows 108 + 72 / 109 + 70,
+// 62 rows 126 + 79 / 119 + 77. 32 / 64 rows, gate/up: 128 of 2048 x 768 with 10
+// rows 44 / 44, 31 rows 61 / 52; 8 of 4096 x 14336 with 32 rows 137 / 110. (256
+// rows: 1024 on average 1478 against 1496, but down 834 against 803.) 4-bit rows
+// (gate/up, 64 / 128 / 256): 8 x 4096 x 14336 with
 // 8 rows 92 / 92 / 92, 83 rows 145 / 111 / 113, 175 rows 222 / 161 / 143, 1024
 // rows 735 / 586 / 571; 128 x 2048 x 768 with 128 rows 91 / 71 / 61; 64 x 4096 x
 // 1408 with two experts taking most rows, mean 10: 45 / 46 / 54, mean 31: 86 /
@@ -428,7 +446,7 @@ int mx_tile_rows(int A, int E, bool a4)
     const int64_t mean = ((int64_t)A + E - 1) / E;
     if (a4)
         return mean <= 20 ? 64 : mean <= 100 ? 128 : 256;
-    return mean <= 20 ? 32 : mean <= 40 ? 64 : 128;
+    return mean <= 20 ? 32 : mean <= 50 ? 64 : 128;
 }
 
 }  // namespace
@@ -436,7 +454,7 @@ int mx_tile_rows(int A, int E, bool a4)
 int mx_down_split(int A, int E, int d, int f, int cus)
 {
     // K splits of the down GEMM: up to four, until there are three tiles per
-    // compute unit (two run there at a time), while each part keeps 1024 k.
+    // compute unit (two or three run there at a time), while each part keeps 1024 k.
     // Measured with one / two / four (down GEMM and combine, us): 8 experts of
     // 4096 x 14336, 32 tokens - / 58 / 59, 333 tokens - / 103 / 96, 2047 tokens
     // 470 / 454 / 483, 4096 tokens 842 / 859 / -; 128 experts of 2048 x 768 lose
@@ -464,16 +482,16 @@ hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s)
                              : launch_shape<256, 2, 3, true, true>(a, s);
     }
     const int rows = mx_tile_rows(a.A_max, a.E, false);
-    return rows == 32   ? launch_shape<32, 1, 5, false, true>(a, s)
-           : rows == 64 ? launch_shape<64, 1, 4, false, true>(a, s)
+    return rows == 32   ? launch_shape<32, 1, 4, false, true>(a, s)
+           : rows == 64 ? launch_shape<64, 1, 3, false, true>(a, s)
                         : launch_shape<128, 1, 3, false, true>(a, s);
 }
 
 hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s)
 {
     const int rows = mx_tile_rows(a.A_max, a.E, false);
-    return rows == 32   ? launch_shape<32, 1, 5, false, false>(a, s)
-           : rows == 64 ? launch_shape<64, 1, 4, false, false>(a, s)
+    return rows == 32   ? launch_shape<32, 1, 4, false, false>(a, s)
+           : rows == 64 ? launch_shape<64, 1, 3, false, false>(a, s)
                         : launch_shape<128, 1, 3, false, false>(a, s);
 }
 
