@@ -190,12 +190,34 @@ def _on_device_of(t, fn, *args):
         return fn(*args)
 
 
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensor")
+
+
+def _new_output(shape, dtype, device, stream):
+    """An output of a call on `stream` (None: the current one). It is memory of
+    that stream's own pool: what the allocator hands out of the current
+    stream's pool may still be in use by kernels queued there, which nothing
+    orders before `stream`. The current stream is recorded as a user, since
+    the caller goes on there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def quantize_mxfp4(w, stream=None):
     """(codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]) of a 2-D
     bf16 or fp32 device tensor whose rows are contiguous (they may be slices of
     longer ones): the 4-bit microscaled codes a layer built with
     FLAG_MXFP4_WEIGHTS keeps. cols must be a multiple of 32. The work is
-    enqueued on `stream`, by default the current one."""
+    enqueued on `stream`, by default the current one; a given stream must
+    already be ordered behind the work that makes w."""
     import torch
 
     bf16 = w.dtype == torch.bfloat16
@@ -205,15 +227,15 @@ def quantize_mxfp4(w, stream=None):
     row_stride, step = w.stride()
     if cols % 32 != 0 or (cols > 1 and step != 1) or (rows > 1 and row_stride < cols):
         raise ValueError("rows must be contiguous, a multiple of 32 long, and must not overlap")
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=w.device)
+    _check_stream(stream, w.device)
+    codes = _new_output((rows, cols // 2), torch.uint8, w.device, stream)
+    scales = _new_output((rows, cols // 32), torch.uint8, w.device, stream)
     if rows == 0 or cols == 0:
         return codes, scales
     st = _on_device_of(w, colibri_moe_quantize_mxfp4, w.data_ptr(), BF16 if bf16 else F32, rows, cols,
                        row_stride if rows > 1 else cols, codes.data_ptr(), scales.data_ptr(), _stream_of(w, stream))
-    if stream is not None:  # the tensors belong to the current stream, their memory waits for this one
-        for t in (w, codes, scales):
-            t.record_stream(stream)
+    if stream is not None:  # w's memory is not used again before this stream is done with it
+        w.record_stream(stream)
     if st != OK:
         raise ColibriError("colibri_moe_quantize_mxfp4", st)
     return codes, scales
@@ -223,7 +245,8 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     """The values [rows][cols] (bf16 by default, or fp32) of 4-bit microscaled
     rows: contiguous uint8 device tensors codes [rows][cols/2] and scales
     [rows][cols/32]. Exact. The work is enqueued on `stream`, by default the
-    current one."""
+    current one; a given stream must already be ordered behind the work that
+    makes the codes and scales."""
     import torch
 
     bf16 = dtype is None or dtype == torch.bfloat16
@@ -235,13 +258,14 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     rows, cols = codes.shape[0], codes.shape[1] * 2
     if scales.device != codes.device or scales.shape[0] != rows or scales.shape[1] * 32 != cols:
         raise ValueError("codes [rows][cols/2] and scales [rows][cols/32] do not belong together")
-    out = torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32, device=codes.device)
+    _check_stream(stream, codes.device)
+    out = _new_output((rows, cols), torch.bfloat16 if bf16 else torch.float32, codes.device, stream)
     if rows == 0 or cols == 0:
         return out
     st = _on_device_of(codes, colibri_moe_dequantize_mxfp4, codes.data_ptr(), scales.data_ptr(), rows, cols,
                        BF16 if bf16 else F32, out.data_ptr(), _stream_of(codes, stream))
     if stream is not None:
-        for t in (codes, scales, out):
+        for t in (codes, scales):
             t.record_stream(stream)
     if st != OK:
         raise ColibriError("colibri_moe_dequantize_mxfp4", st)
