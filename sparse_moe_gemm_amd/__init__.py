@@ -144,34 +144,6 @@ def colibri_moe_quantize_fp8(w_ptr: int, rows: int, cols: int, codes_ptr: int, s
                                           ctypes.c_void_p(scales_ptr), ctypes.c_void_p(hip_stream))
 
 
-def quantize_fp8(w, stream=None):
-    """(codes uint8 [rows][cols], scales fp32 [rows]) of a contiguous bf16
-    device tensor [rows][cols]: the 8-bit codes a layer built with
-    FLAG_FP8_WEIGHTS keeps."""
-    import torch
-
-    if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_cuda or not w.is_contiguous():
-        raise TypeError("w must be a contiguous 2-D bfloat16 device tensor")
-    rows, cols = w.shape
-    codes = torch.empty(rows, cols, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(rows, dtype=torch.float32, device=w.device)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    st = colibri_moe_quantize_fp8(w.data_ptr(), rows, cols, codes.data_ptr(), scales.data_ptr(), s.cuda_stream)
-    if st != OK:
-        raise ColibriError("colibri_moe_quantize_fp8", st)
-    return codes, scales
-
-
-def colibri_moe_quantize_mxfp4(w_ptr: int, dtype: int, rows: int, cols: int, row_stride: int, codes_ptr: int,
-                               scales_ptr: int, hip_stream: int = 0) -> int:
-    return lib().colibri_moe_quantize_mxfp4(w_ptr, dtype, rows, cols, row_stride, codes_ptr, scales_ptr, hip_stream)
-
-
-def colibri_moe_dequantize_mxfp4(codes_ptr: int, scales_ptr: int, rows: int, cols: int, dtype: int, out_ptr: int,
-                                 hip_stream: int = 0) -> int:
-    return lib().colibri_moe_dequantize_mxfp4(codes_ptr, scales_ptr, rows, cols, dtype, out_ptr, hip_stream)
-
-
 def _stream_of(t, stream):
     """Handle of `stream`, or of the current stream of t's device (its raw
     handle: building a Stream object costs as much as the launch)."""
@@ -209,6 +181,39 @@ def _new_output(shape, dtype, device, stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+def quantize_fp8(w, stream=None):
+    """(codes uint8 [rows][cols], scales fp32 [rows]) of a contiguous bf16
+    device tensor [rows][cols]: the 8-bit codes a layer built with
+    FLAG_FP8_WEIGHTS keeps. Runs on `stream`, by default the current one, and
+    waits for it; a given stream must already be ordered behind the work that
+    makes w."""
+    import torch
+
+    if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_cuda or not w.is_contiguous():
+        raise TypeError("w must be a contiguous 2-D bfloat16 device tensor")
+    rows, cols = w.shape
+    _check_stream(stream, w.device)
+    codes = _new_output((rows, cols), torch.uint8, w.device, stream)
+    scales = _new_output((rows,), torch.float32, w.device, stream)
+    st = _on_device_of(w, colibri_moe_quantize_fp8, w.data_ptr(), rows, cols, codes.data_ptr(), scales.data_ptr(),
+                       _stream_of(w, stream))
+    if stream is not None:
+        w.record_stream(stream)
+    if st != OK:
+        raise ColibriError("colibri_moe_quantize_fp8", st)
+    return codes, scales
+
+
+def colibri_moe_quantize_mxfp4(w_ptr: int, dtype: int, rows: int, cols: int, row_stride: int, codes_ptr: int,
+                               scales_ptr: int, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_quantize_mxfp4(w_ptr, dtype, rows, cols, row_stride, codes_ptr, scales_ptr, hip_stream)
+
+
+def colibri_moe_dequantize_mxfp4(codes_ptr: int, scales_ptr: int, rows: int, cols: int, dtype: int, out_ptr: int,
+                                 hip_stream: int = 0) -> int:
+    return lib().colibri_moe_dequantize_mxfp4(codes_ptr, scales_ptr, rows, cols, dtype, out_ptr, hip_stream)
 
 
 def quantize_mxfp4(w, stream=None):

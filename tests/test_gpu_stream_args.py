@@ -44,3 +44,20 @@ def test_mxfp4_quantizers_on_a_given_stream():
         torch.cuda.synchronize()
         queued.check(r)
         assert torch.equal(codes, want_c) and torch.equal(scales, want_s) and torch.equal(values, want_v), r
+
+
+def test_fp8_quantizer_on_a_given_stream():
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    w = torch.randn(512, 4096, device="cuda").bfloat16()
+    want_c, want_s = cm.quantize_fp8(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for r in range(4):
+        queued = Queued((want_c, want_s))
+        codes, scales = cm.quantize_fp8(w, stream=side)
+        torch.cuda.synchronize()
+        queued.check(r)
+        assert torch.equal(codes, want_c) and torch.equal(scales, want_s), r

@@ -60,3 +60,19 @@ def test_a_stream_of_another_device_is_refused(dev, monkeypatch):
         cm.quantize_mxfp4(tensor(dev, (4, 64), torch.bfloat16), stream=s)
     with pytest.raises(ValueError):
         cm.dequantize_mxfp4(tensor(dev, (4, 32), torch.uint8), tensor(dev, (4, 2), torch.uint8), stream=s)
+
+
+def test_quantize_fp8_outputs_belong_to_the_stream_that_writes_them(dev, monkeypatch):
+    calls = []
+    monkeypatch.setattr(cm, "colibri_moe_quantize_fp8", lambda *a: calls.append(a) or cm.OK)
+    w = tensor(dev, (4, 64), torch.bfloat16)
+    s = fake_device.Stream(0x54)
+    codes, scales = cm.quantize_fp8(w, stream=s)
+    assert calls[-1][-3:] == (codes.ptr, scales.ptr, 0x54)
+    check_outputs(dev, (codes, scales), s)
+    assert s in w.recorded
+    check_outputs(dev, cm.quantize_fp8(w), dev.current)
+    assert calls[-1][-1] == 0
+    with pytest.raises(ValueError):
+        cm.quantize_fp8(w, stream=fake_device.Stream(0x55, index=1))
+    assert len(calls) == 2
