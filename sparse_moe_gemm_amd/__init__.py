@@ -355,7 +355,9 @@ class MoELayer:
 
     def forward(self, x, y=None, routing: dict | None = None, static_scratch: bool = False):
         """y [T][d] = layer(x). ``routing`` (from routing_buffers) receives the
-        routing outputs; missing keys are not written. static_scratch: call
+        routing outputs; missing keys are not written. Runs on the handle's
+        stream, which must already be ordered behind the work that makes x and
+        behind earlier uses of a given y or routing buffer. static_scratch: call
         colibri_moe_forward_static (working memory in the library's fixed
         per-GPU array instead of the handle's)."""
         return self._call(colibri_moe_forward_static if static_scratch else colibri_moe_forward, x, y, routing)
@@ -370,8 +372,19 @@ class MoELayer:
         if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != self.d or not x.is_contiguous():
             raise TypeError("x must be a contiguous [T][d] tensor of the layer dtype")
         T = x.shape[0]
+        # The kernels run on the handle's stream: when that is not the current
+        # one, a y made here is memory of its pool, and the memory of the
+        # caller's tensors is not used again before it is done with them.
+        other = torch._C._cuda_getCurrentRawStream(x.device.index) != self.stream.cuda_stream
+        mine = [x, *(routing or {}).values()]
         if y is None:
-            y = torch.empty_like(x)
+            y = _new_output(x.shape, x.dtype, x.device, self.stream if other else None)
+        else:
+            mine.append(y)
+        if other:
+            for t in mine:
+                if t is not None:
+                    t.record_stream(self.stream)
         r = None
         if routing is not None:
             r = Routing(*[routing[n].data_ptr() if routing.get(n) is not None else None

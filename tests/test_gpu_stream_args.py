@@ -61,3 +61,28 @@ def test_fp8_quantizer_on_a_given_stream():
         torch.cuda.synchronize()
         queued.check(r)
         assert torch.equal(codes, want_c) and torch.equal(scales, want_s), r
+
+
+@pytest.mark.parametrize("entry", ["forward", "forward_few"])
+def test_layer_of_another_stream(entry):
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+    import synth
+    from moe_case import to_dev
+
+    cfg = synth.LayerConfig("other-stream", 16, 512, 8, 2, 512, "bf16")
+    inp = synth.make_inputs(cfg)
+    layer = cm.MoELayer(to_dev(inp["w_router"]), to_dev(inp["b_router"]), to_dev(inp["w_gate"]), to_dev(inp["w_up"]),
+                        to_dev(inp["w_down"]), cfg.k, max_tokens=16, flags=cm.FLAG_ASYNC, stream=torch.cuda.Stream())
+    x = to_dev(inp["x"])
+    torch.cuda.synchronize()
+    want = getattr(layer, entry)(x, torch.empty_like(x))
+    torch.cuda.synchronize()
+    for r in range(4):
+        queued = Queued((x,))
+        y = getattr(layer, entry)(x)
+        torch.cuda.synchronize()
+        queued.check(r)
+        assert torch.equal(y, want), r
+    layer.close()

@@ -76,3 +76,32 @@ def test_quantize_fp8_outputs_belong_to_the_stream_that_writes_them(dev, monkeyp
     with pytest.raises(ValueError):
         cm.quantize_fp8(w, stream=fake_device.Stream(0x55, index=1))
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("entry", ["forward", "forward_few"])
+def test_layer_outputs_belong_to_the_handles_stream(dev, monkeypatch, entry):
+    calls = []
+
+    def call(handle, x, T, y, r):
+        calls.append(y)
+        return cm.OK
+
+    monkeypatch.setattr(cm, f"colibri_moe_{entry}", call)
+    layer = cm.MoELayer.__new__(cm.MoELayer)
+    layer._torch, layer.handle, layer.dtype = torch, 0, torch.bfloat16
+    layer.d, layer.E, layer.f, layer.k, layer.max_tokens = 64, 8, 128, 2, 16
+    layer.stream = fake_device.Stream(0x56)
+    x = tensor(dev, (4, 64), torch.bfloat16)
+    y = getattr(layer, entry)(x)
+    assert calls == [y.ptr]
+    check_outputs(dev, (y,), layer.stream)
+    assert layer.stream in x.recorded
+    # a given y and routing buffers stay where they are; their memory too waits for the stream
+    mine, ids = tensor(dev, (4, 64), torch.bfloat16), tensor(dev, (4, 2), torch.int32)
+    assert getattr(layer, entry)(x, mine, {"topk_ids": ids, "inv": None}) is mine
+    assert layer.stream in mine.recorded and layer.stream in ids.recorded
+    # on the handle's own stream nothing is recorded
+    dev.current = layer.stream
+    x = tensor(dev, (4, 64), torch.bfloat16)
+    y = getattr(layer, entry)(x)
+    assert y.pool is layer.stream and not y.recorded and not x.recorded
