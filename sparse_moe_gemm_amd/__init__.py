@@ -334,6 +334,7 @@ class MoELayer:
             raise TypeError("b_router must be a float32 device tensor")
         wts = Weights(w_router.data_ptr(), None if b_router is None else b_router.data_ptr(),
                       w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
+        self.device = w_router.device
         self.stream = stream if stream is not None else torch.cuda.current_stream()
         st, h = colibri_moe_init(self.cfg, wts, self.stream.cuda_stream)
         if st != OK:
@@ -369,30 +370,44 @@ class MoELayer:
 
     def _call(self, fn, x, y, routing):
         torch = self._torch
-        if x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != self.d or not x.is_contiguous():
-            raise TypeError("x must be a contiguous [T][d] tensor of the layer dtype")
+        if (x.dtype != self.dtype or x.dim() != 2 or x.shape[1] != self.d or not x.is_contiguous()
+                or x.device != self.device):
+            raise TypeError("x must be a contiguous [T][d] tensor of the layer dtype on the layer's device")
         T = x.shape[0]
+        if y is not None and (y.dtype != self.dtype or not y.is_contiguous() or y.device != self.device
+                              or y.numel() < T * self.d):
+            raise TypeError("y must be a contiguous [T][d] tensor of the layer dtype on the layer's device")
         # The kernels run on the handle's stream: when that is not the current
         # one, a y made here is memory of its pool, and the memory of the
         # caller's tensors is not used again before it is done with them.
         other = torch._C._cuda_getCurrentRawStream(x.device.index) != self.stream.cuda_stream
-        mine = [x, *(routing or {}).values()]
+        given = y
         if y is None:
             y = _new_output(x.shape, x.dtype, x.device, self.stream if other else None)
-        else:
-            mine.append(y)
         if other:
-            for t in mine:
+            for t in (x, given, *((routing or {}).get(n) for n, _ in Routing._fields_)):
                 if t is not None:
                     t.record_stream(self.stream)
         r = None
         if routing is not None:
+            self._check_routing(routing, T)
             r = Routing(*[routing[n].data_ptr() if routing.get(n) is not None else None
                           for n, _ in Routing._fields_])
         st = fn(self.handle, x.data_ptr(), T, y.data_ptr(), r)
         if st != OK:
             raise ColibriError(fn.__name__, st)
         return y
+
+    def _check_routing(self, routing, T):
+        torch = self._torch
+        A, f32, i32 = T * self.k, torch.float32, torch.int32
+        for n, dtype, size in (("logits", f32, T * self.E), ("topk_ids", i32, A), ("topk_w", f32, A),
+                               ("expert_counts", i32, self.E), ("expert_offsets", i32, self.E + 1),
+                               ("perm", i32, A), ("perm_slot", i32, A), ("inv", i32, A)):
+            t = routing.get(n)
+            if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.device != self.device
+                                  or t.numel() < size):
+                raise TypeError(f"{n} must be a contiguous {dtype} tensor of {size} elements on the layer's device")
 
     def stage_times(self) -> dict:
         return dict(zip(STAGES, colibri_moe_stage_times(self.handle)))

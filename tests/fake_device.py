@@ -80,3 +80,14 @@ class Device:
 
     def of(self, ptr):
         return next(t for t in self.made if t.ptr == ptr)
+
+
+def layer(dev, stream=None, dtype=torch.bfloat16, d=64, E=8, f=128, k=2, max_tokens=16):
+    """A MoELayer without a handle behind it."""
+    import sparse_moe_gemm_amd as cm
+
+    out = cm.MoELayer.__new__(cm.MoELayer)
+    out._torch, out.handle, out.dtype, out.device = torch, 0, dtype, torch.device("cuda", 0)
+    out.d, out.E, out.f, out.k, out.max_tokens = d, E, f, k, max_tokens
+    out.stream = stream if stream is not None else dev.current
+    return out

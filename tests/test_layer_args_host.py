@@ -1,0 +1,76 @@
+"""Tensors that do not fit a call are refused by the binding before their
+pointers reach the library, on stand-ins for device tensors."""
+import pytest
+import torch
+
+import fake_device
+import sparse_moe_gemm_amd as cm
+
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+ENTRIES = ["forward", "forward_few"]
+
+
+@pytest.fixture
+def dev(monkeypatch):
+    return fake_device.Device(monkeypatch)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    for e in ENTRIES:
+        monkeypatch.setattr(cm, f"colibri_moe_{e}", lambda *a: seen.append(a) or cm.OK)
+    return seen
+
+
+def tensor(dev, shape, dtype, index=0, contiguous=True):
+    t = fake_device.Tensor(shape, dtype, dev.current, index)
+    t.is_contiguous = lambda: contiguous
+    return t
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_x_and_y_that_do_not_fit(dev, calls, entry):
+    run = getattr(fake_device.layer(dev), entry)
+    x = tensor(dev, (4, 64), BF16)
+    with pytest.raises(TypeError):
+        run(torch.zeros(4, 64, dtype=BF16))  # not on a GPU
+    for bad in (tensor(dev, (4, 64), F32), tensor(dev, (4, 65), BF16), tensor(dev, (4, 1, 64), BF16),
+                tensor(dev, (4, 64), BF16, index=1), tensor(dev, (4, 64), BF16, contiguous=False)):
+        with pytest.raises(TypeError):
+            run(bad)
+    with pytest.raises(TypeError):
+        run(x, torch.zeros(4, 64, dtype=BF16))
+    for bad in (tensor(dev, (4, 64), F32), tensor(dev, (3, 64), BF16), tensor(dev, (4, 64), BF16, index=1),
+                tensor(dev, (4, 64), BF16, contiguous=False)):
+        with pytest.raises(TypeError):
+            run(x, bad)
+    assert not calls
+    y = tensor(dev, (6, 64), BF16)  # rows behind the call's tokens are left alone
+    assert run(x, y) is y and len(calls) == 1
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("name,dtype,size", [
+    ("logits", F32, 32), ("topk_ids", I32, 8), ("topk_w", F32, 8), ("expert_counts", I32, 8),
+    ("expert_offsets", I32, 9), ("perm", I32, 8), ("perm_slot", I32, 8), ("inv", I32, 8)])
+def test_routing_buffers_that_do_not_fit(dev, calls, entry, name, dtype, size):
+    run = getattr(fake_device.layer(dev), entry)
+    x = tensor(dev, (4, 64), BF16)
+    other = I32 if dtype is F32 else F32
+    for bad in (tensor(dev, (size - 1,), dtype), tensor(dev, (size,), other), tensor(dev, (size,), dtype, index=1),
+                tensor(dev, (size,), dtype, contiguous=False), torch.zeros(size, dtype=dtype)):
+        with pytest.raises(TypeError, match=name):
+            run(x, None, {name: bad})
+    assert not calls
+    run(x, None, {name: tensor(dev, (size,), dtype)})
+    run(x, None, {"logits": None, "inv": None, "note": "not a routing output"})
+    assert len(calls) == 2
+
+
+def test_the_layers_own_buffers_fit(dev, calls):
+    layer = fake_device.layer(dev)
+    layer.forward_few(tensor(dev, (4, 64), BF16), None, layer.routing_buffers(4))
+    layer.stream = fake_device.Stream(0x60)
+    layer.forward_few(tensor(dev, (4, 64), BF16), None, {**layer.routing_buffers(4), "note": "not a routing output"})
+    assert len(calls) == 2

@@ -87,10 +87,7 @@ def test_layer_outputs_belong_to_the_handles_stream(dev, monkeypatch, entry):
         return cm.OK
 
     monkeypatch.setattr(cm, f"colibri_moe_{entry}", call)
-    layer = cm.MoELayer.__new__(cm.MoELayer)
-    layer._torch, layer.handle, layer.dtype = torch, 0, torch.bfloat16
-    layer.d, layer.E, layer.f, layer.k, layer.max_tokens = 64, 8, 128, 2, 16
-    layer.stream = fake_device.Stream(0x56)
+    layer = fake_device.layer(dev, stream=fake_device.Stream(0x56))
     x = tensor(dev, (4, 64), torch.bfloat16)
     y = getattr(layer, entry)(x)
     assert calls == [y.ptr]
