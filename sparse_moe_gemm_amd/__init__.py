@@ -330,8 +330,12 @@ class MoELayer:
         for t in (w_router, w_gate, w_up, w_down):
             if not t.is_cuda or not t.is_contiguous() or t.dtype != dt:
                 raise TypeError("weights must be contiguous device tensors of one dtype")
+        if (tuple(w_gate.shape), tuple(w_up.shape), tuple(w_down.shape)) != ((E, f, d), (E, f, d), (E, d, f)):
+            raise ValueError("w_gate and w_up must be [E][f][d], w_down [E][d][f], for a w_router of [d][E]")
         if b_router is not None and (b_router.dtype != torch.float32 or not b_router.is_cuda):
             raise TypeError("b_router must be a float32 device tensor")
+        if b_router is not None and (not b_router.is_contiguous() or b_router.numel() != E):
+            raise ValueError("b_router must be contiguous and hold E values")
         wts = Weights(w_router.data_ptr(), None if b_router is None else b_router.data_ptr(),
                       w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
         self.device = w_router.device

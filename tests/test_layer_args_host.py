@@ -74,3 +74,29 @@ def test_the_layers_own_buffers_fit(dev, calls):
     layer.stream = fake_device.Stream(0x60)
     layer.forward_few(tensor(dev, (4, 64), BF16), None, {**layer.routing_buffers(4), "note": "not a routing output"})
     assert len(calls) == 2
+
+
+def weights(dev, d=64, E=8, f=128, index=0):
+    shapes = dict(w_router=(d, E), b_router=(E,), w_gate=(E, f, d), w_up=(E, f, d), w_down=(E, d, f))
+    return {n: tensor(dev, v, F32 if n == "b_router" else BF16, index) for n, v in shapes.items()}
+
+
+def test_weights_that_do_not_belong_together(dev, monkeypatch):
+    made = []
+    monkeypatch.setattr(cm, "colibri_moe_init", lambda *a: made.append(a) or (cm.OK, 7))
+    monkeypatch.setattr(cm, "colibri_moe_free", lambda h: cm.OK)
+    for name, shapes in dict(w_gate=[(7, 128, 64), (8, 128, 32)], w_up=[(8, 64, 64), (8, 64, 128), (7, 128, 64)],
+                             w_down=[(8, 128, 64), (8, 64, 64)], b_router=[(7,), (16,)]).items():
+        for shape in shapes:
+            w = weights(dev)
+            w[name] = tensor(dev, shape, w[name].dtype)
+            with pytest.raises(ValueError):
+                cm.MoELayer(**w, top_k=2, max_tokens=16)
+    w = weights(dev)
+    w["b_router"].is_contiguous = lambda: False
+    with pytest.raises(ValueError):
+        cm.MoELayer(**w, top_k=2, max_tokens=16)
+    assert not made
+    cm.MoELayer(**weights(dev), top_k=2, max_tokens=16)
+    cm.MoELayer(**{**weights(dev), "b_router": None}, top_k=2, max_tokens=16)
+    assert len(made) == 2
