@@ -311,7 +311,9 @@ class MoELayer:
 
     Weight tensors are CUDA (HIP) tensors: w_router [d][E], b_router [E] fp32 or
     None, w_gate/w_up [E][f][d], w_down [E][d][f], all torch.bfloat16 or all
-    torch.float32.
+    torch.float32, on the device the layer is to run on. Its calls run on
+    `stream`, by default that device's current one; a given stream must already
+    be ordered behind the work that makes the weights.
     """
 
     def __init__(self, w_router, b_router, w_gate, w_up, w_down, top_k: int, max_tokens: int,
@@ -328,26 +330,27 @@ class MoELayer:
         self.dtype = dt
         self.cfg = Config(d, f, E, self.k, self.max_tokens, BF16 if dt == torch.bfloat16 else F32, flags)
         for t in (w_router, w_gate, w_up, w_down):
-            if not t.is_cuda or not t.is_contiguous() or t.dtype != dt:
-                raise TypeError("weights must be contiguous device tensors of one dtype")
+            if not t.is_cuda or not t.is_contiguous() or t.dtype != dt or t.device != w_router.device:
+                raise TypeError("weights must be contiguous tensors of one dtype on one device")
         if (tuple(w_gate.shape), tuple(w_up.shape), tuple(w_down.shape)) != ((E, f, d), (E, f, d), (E, d, f)):
             raise ValueError("w_gate and w_up must be [E][f][d], w_down [E][d][f], for a w_router of [d][E]")
-        if b_router is not None and (b_router.dtype != torch.float32 or not b_router.is_cuda):
-            raise TypeError("b_router must be a float32 device tensor")
+        if b_router is not None and (b_router.dtype != torch.float32 or b_router.device != w_router.device):
+            raise TypeError("b_router must be a float32 tensor on the weights' device")
         if b_router is not None and (not b_router.is_contiguous() or b_router.numel() != E):
             raise ValueError("b_router must be contiguous and hold E values")
         wts = Weights(w_router.data_ptr(), None if b_router is None else b_router.data_ptr(),
                       w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
         self.device = w_router.device
-        self.stream = stream if stream is not None else torch.cuda.current_stream()
-        st, h = colibri_moe_init(self.cfg, wts, self.stream.cuda_stream)
+        _check_stream(stream, self.device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        st, h = _on_device_of(w_router, colibri_moe_init, self.cfg, wts, self.stream.cuda_stream)
         if st != OK:
             raise ColibriError("colibri_moe_init", st)
         self.handle = h
 
     def routing_buffers(self, T: int) -> dict:
         torch = self._torch
-        dev = "cuda"
+        dev = self.device
         A = T * self.k
         return dict(logits=torch.empty(T, self.E, dtype=torch.float32, device=dev),
                     topk_ids=torch.empty(T, self.k, dtype=torch.int32, device=dev),

@@ -54,12 +54,13 @@ class Device:
 
     def __init__(self, monkeypatch):
         self.current = Stream(0)
+        self.index = 0  # of the current device
         self.made = []
 
         def empty(*shape, dtype=None, device=None, **_):
             if len(shape) == 1 and not isinstance(shape[0], int):
                 shape = shape[0]
-            t = Tensor(shape, dtype, self.current)
+            t = Tensor(shape, dtype, self.current, torch.device(device or "cuda").index or 0)
             self.made.append(t)
             return t
 
@@ -71,11 +72,22 @@ class Device:
             finally:
                 self.current = before
 
+        @contextlib.contextmanager
+        def device(d):
+            before, self.index = self.index, torch.device(d).index
+            try:
+                yield
+            finally:
+                self.index = before
+
         monkeypatch.setattr(torch, "empty", empty)
-        monkeypatch.setattr(torch, "empty_like", lambda t, **_: empty(t.shape, dtype=t.dtype))
+        monkeypatch.setattr(torch, "empty_like", lambda t, **_: empty(t.shape, dtype=t.dtype, device=t.device))
         monkeypatch.setattr(torch.cuda, "stream", stream)
-        monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: self.current)
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda d=None: self.current if torch.device(d or "cuda").index in (None, 0)
+                            else Stream(0x1000, torch.device(d).index))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.index)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda _: self.current.cuda_stream, raising=False)
 
     def of(self, ptr):

@@ -100,3 +100,22 @@ def test_weights_that_do_not_belong_together(dev, monkeypatch):
     cm.MoELayer(**weights(dev), top_k=2, max_tokens=16)
     cm.MoELayer(**{**weights(dev), "b_router": None}, top_k=2, max_tokens=16)
     assert len(made) == 2
+
+
+def test_layer_lives_on_its_weights_device(dev, monkeypatch):
+    made = []
+    monkeypatch.setattr(cm, "colibri_moe_init", lambda c, w, s: made.append((dev.index, s)) or (cm.OK, 7))
+    monkeypatch.setattr(cm, "colibri_moe_free", lambda h: cm.OK)
+    layer = cm.MoELayer(**weights(dev, index=1), top_k=2, max_tokens=16)
+    assert made == [(1, 0x1000)] and dev.index == 0
+    assert all(t.device.index == 1 for t in layer.routing_buffers(4).values())
+    cm.MoELayer(**weights(dev, index=1), top_k=2, max_tokens=16, stream=fake_device.Stream(0x61, index=1))
+    assert made[1:] == [(1, 0x61)]
+    for name in ("w_gate", "w_up", "w_down", "b_router"):
+        w = weights(dev, index=1)
+        w[name] = weights(dev)[name]
+        with pytest.raises(TypeError):
+            cm.MoELayer(**w, top_k=2, max_tokens=16)
+    with pytest.raises(ValueError):
+        cm.MoELayer(**weights(dev, index=1), top_k=2, max_tokens=16, stream=fake_device.Stream(0x62))
+    assert len(made) == 2
