@@ -118,9 +118,9 @@ bool aligned16(const void* p)
     return ((uintptr_t)p & 15u) == 0;
 }
 
-// Makes a device current for as long as it lives. The handle's kernels run on
-// the handle's device, whichever the calling thread works on (a NULL stream
-// means the current device's).
+// Makes a device current for as long as it lives. The handle's kernels run, and
+// are waited for, on the handle's device, whichever the calling thread works on
+// (a NULL stream means the current device's).
 struct OnDevice {
     int before = -1;
     explicit OnDevice(int device)
@@ -787,6 +787,7 @@ colibri_moe_status_t colibri_moe_free(colibri_moe_t* h)
         if (!g_live.erase(h))
             return COLIBRI_MOE_ERR_INVALID_ARG;
     }
+    const OnDevice on(h->device);
     const bool ok = hipStreamSynchronize(h->stream) == hipSuccess;
     release(h);
     return ok ? COLIBRI_MOE_OK : COLIBRI_MOE_ERR_HIP;
