@@ -543,6 +543,14 @@ __host__ __device__ constexpr int down_groups(int fmt)
     return fmt == kMx4 ? 4 : 2;
 }
 
+// What the low parts of h add to a sum of weights times h. An infinite weight
+// decides such a sum by the high parts alone: times a low part it would give
+// NaN (0 * inf) or the opposite infinity.
+__device__ __forceinline__ float low_sum(float v)
+{
+    return fabsf(v) < INFINITY ? v : 0.f;
+}
+
 // Loads of B units of the down kernel: weights and scales of both 16-row
 // halves, and the token fragments of h (lanes whose token did not choose the
 // expert load nothing and hold zeros). H = 2: high and low parts apart, for 16
@@ -688,6 +696,33 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
                     for (int p = 0; p < H; ++p)
                         acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(t.x[b][s][p]), acc[h], 0, 0, 0);
                 }
+            // A sum that is not finite is taken again without the low parts
+            // (low_sum). H = 1 keeps the parts' sums apart to the end.
+            if constexpr (H == 2) {
+                float bad = 0.f;
+#pragma unroll
+                for (int h = 0; h < W; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        bad = fmaf(acc[h][i], 0.f, bad);
+                if (__ballot(bad != 0.f) != 0) {  // NaN: some sum is not finite
+#pragma unroll
+                    for (int h = 0; h < W; ++h) {
+                        floatx4 hi = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < M; ++s) {
+                            float sc = FMT == kMx4 ? mx_scale(t.mx[FMT == kMx4 ? b : 0][h]) : t.sc[FMT == kFp8 ? b : 0][h];
+                            if constexpr (FMT != kBf16)  // converts again: fragments kept for this would spill
+                                asm volatile("" : "+v"(sc));
+                            hi = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unit_frag<FMT>(t.w[b][h], s, sc),
+                                                                         as_bf16x8(t.x[b][s][0]), hi, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[h][i] = fabsf(acc[h][i]) < INFINITY ? acc[h][i] : hi[i];
+                    }
+                }
+            }
             // only the tokens that chose this expert take its rows (whose
             // weights may be infinite or NaN)
 #pragma unroll
@@ -727,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs g)
     if (tid < W * 256)
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
-            sum += H == 1 ? red[w][tid] + red[w][tid ^ 32] : red[w][tid];  // ^ 32: eight columns on
+            sum += H == 1 ? red[w][tid] + low_sum(red[w][tid ^ 32]) : red[w][tid];  // ^ 32: eight columns on
     if (g.split > 1) {
         // Parts and counts are accessed at device scope (written through and
         // read past the XCDs' separate L2s), ordered by the wait for the stores
