@@ -57,6 +57,13 @@ __device__ __forceinline__ float silu(float z)
     return z / (1.0f + __expf(-z));
 }
 
+// SiLU with the hardware reciprocal (about 1 ulp) instead of an IEEE divide;
+// the result is rounded to bf16 right after.
+__device__ __forceinline__ float silu_rcp(float z)
+{
+    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
 // Most rows any expert holds in this call (offsets [E+1]), the same value in
 // every lane of the wave. Calls that enqueue both GEMM paths let each kernel
 // decide from it, on the device, whether the call is its own.

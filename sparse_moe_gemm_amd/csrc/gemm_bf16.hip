@@ -33,6 +33,7 @@
 // n-tile; workgroups are spread over the 8 XCDs round robin, so the tiles one
 // XCD runs together share a few token and weight panels in its L2.
 #include "common.hpp"
+#include "lds_dma.hpp"
 #include "tiles.hpp"
 
 namespace cmoe {
@@ -51,20 +52,6 @@ constexpr int kAhead = kRing - 1;       // stages in flight ahead of the one mul
 __device__ __forceinline__ int swz(int row, int chunk)
 {
     return chunk ^ ((row >> 2) & 3);
-}
-
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-// SiLU with the hardware reciprocal (about 1 ulp) instead of an IEEE divide;
-// the result is rounded to bf16 right after.
-__device__ __forceinline__ float silu_rcp(float z)
-{
-    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p)
-{
-    return (uint32_t)(size_t)(lds_void_t*)p;
 }
 
 // LDS stage layout (one 32-wide K stage of a BM x BN tile):
@@ -113,21 +100,6 @@ __device__ __forceinline__ bf16x8 to_bf16(u32x2 r, float sc)
     return fp8x8_to_bf16(r[0], r[1], sc);
 }
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
-// Buffer resource of a raw byte buffer: base address, size in bytes (loads
-// past it return zeros instead of touching memory), stride 0.
-__device__ __forceinline__ i32x4 make_rsrc(const void* base, uint32_t bytes)
-{
-    const uint64_t a = (uint64_t)(uintptr_t)base;
-    i32x4 r;
-    r[0] = __builtin_amdgcn_readfirstlane((int32_t)(uint32_t)a);
-    r[1] = __builtin_amdgcn_readfirstlane((int32_t)((a >> 32) & 0xFFFFu));
-    r[2] = __builtin_amdgcn_readfirstlane((int32_t)bytes);
-    r[3] = 0x00020000;  // raw buffer, 32-bit data format (CDNA)
-    return r;
-}
-
 // One direct buffer->LDS load: 64 lanes x 16 B from rsrc + voff (per lane) +
 // soff (wave-uniform) into the 1 KiB of LDS at byte address lds (through M0),
 // lane s into slot s. Written as inline assembly on purpose: the ordering of
@@ -136,7 +108,7 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* base, uint32_t bytes)
 // compiler from adding its own full waits before LDS reads, which would drain
 // the stages in flight. M0 is declared clobbered, so the compiler keeps none of
 // its own values there across the load.
-__device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
+__device__ __forceinline__ void dma16(Rsrc rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
                  "s"(soff), "s"(lds)
@@ -147,7 +119,7 @@ __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff, 
 // per-lane byte offsets of its A rows (chunk included) and the k stage.
 template <int A_INS>
 struct LoadSrc {
-    i32x4 rb;
+    Rsrc rb;
     uint32_t aoff[A_INS];
     int kt;
 };
@@ -157,7 +129,7 @@ struct LoadSrc {
 // KB is the number of 1 KiB blocks per 32 weight rows along K (K/16 for bf16
 // weights, K/32 for fp8).
 template <int BM, int BN, bool F8, int A_INS, int B_INS>
-__device__ __forceinline__ void issue_load(int q, const i32x4& ra, const LoadSrc<A_INS>& ls, int KB, int wv,
+__device__ __forceinline__ void issue_load(int q, const Rsrc& ra, const LoadSrc<A_INS>& ls, int KB, int wv,
                                            uint32_t lane16, uint32_t lds)
 {
     using St = Stage<BM, BN, F8>;
@@ -230,7 +202,7 @@ struct FragReader {
 // reads of their k step 1 fragments, are left out. Loads, waits, barriers and
 // the next stage's fragment reads are the same in every variant.
 template <int BM, int BN, int WM, int WN, bool F8, int A_INS, int B_INS, int RG>
-__device__ __forceinline__ void stage(const i32x4& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
+__device__ __forceinline__ void stage(const Rsrc& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
                                       uint32_t lane16, const Stage<BM, BN, F8>* st,
                                       const Stage<BM, BN, F8>* st_next, int wm, int wn, int lane,
                                       bf16x8 (&fa)[WM / 32], typename BFrag<F8>::raw (&fb)[WN / 32],
@@ -403,7 +375,7 @@ struct FragReader16 {
 // next stage starts the next tile) reads them all. An expert's ragged last
 // m-tile then costs far fewer LDS reads than a full one.
 template <int BM, int BN, int WM, int WN, int A_INS, int B_INS, int RG, bool SW>
-__device__ __forceinline__ void stage16(const i32x4& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
+__device__ __forceinline__ void stage16(const Rsrc& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
                                         uint32_t lane16, const Stage<BM, BN, false>* st,
                                         const Stage<BM, BN, false>* st_next, int wm, int wn, int lane,
                                         bf16x8 (&fa)[WM / 16], bf16x8 (&fb)[WN / 16], Acc4 (&acc)[WM / 32][WN / 32],
@@ -519,7 +491,7 @@ struct FragReaderQ8 {
 // as soon as its last MFMA is issued, then the next stage's first A
 // fragments. Half of the loads in each half.
 template <int BM, int BN, int WM, int WN, int A_INS, int B_INS, int RG>
-__device__ __forceinline__ void stage_q8(const i32x4& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
+__device__ __forceinline__ void stage_q8(const Rsrc& ra, const LoadSrc<A_INS>& ls, uint32_t ld_lds, int KB, int wv,
                                          uint32_t lane16, const Stage<BM, BN, false>* st,
                                          const Stage<BM, BN, false>* st_next, int wm, int wn, int lane,
                                          v8i (&fa)[2], v8i (&fb)[WN / 32], const int (&sa)[WM / 32],
@@ -675,10 +647,10 @@ __device__ __forceinline__ void fused_combine(const GemmArgs& g, int row0, int r
 // Buffer resource of a tile's weight panel (blocked layout), bounded by the
 // end of its expert's weights.
 template <int BN>
-__device__ __forceinline__ i32x4 panel_rsrc(const void* b, const Tile& t, int N, int KB)
+__device__ __forceinline__ Rsrc panel_rsrc(const void* b, const Tile& t, int N, int KB)
 {
     const uint8_t* p = (const uint8_t*)b + (((int64_t)t.e * (N / 32) + (int64_t)t.n * (BN / 32)) * KB) * 1024;
-    return make_rsrc(p, (uint32_t)((N / 32 - t.n * (BN / 32)) * KB) * 1024u);
+    return buffer_rsrc(p, (uint32_t)((N / 32 - t.n * (BN / 32)) * KB) * 1024u);
 }
 
 // The K stages of one tile, continuing the stream: stage j multiplies ring
@@ -687,8 +659,8 @@ __device__ __forceinline__ i32x4 panel_rsrc(const void* b, const Tile& t, int N,
 // tile, a reload of this tile's last stage that nobody reads (it keeps the
 // loads per stage, and so every wait count, the same).
 template <int BM, int BN, int WM, int WN, bool F8, bool EPBUF, int A_INS, int B_INS, int RG>
-__device__ __forceinline__ void tile_stages(const i32x4& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
-                                            const i32x4& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
+__device__ __forceinline__ void tile_stages(const Rsrc& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
+                                            const Rsrc& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
                                             uint32_t Kbytes, int KB, int wv, uint32_t lane16,
                                             Ring<BM, BN, F8, EPBUF>& ring, uint32_t ring0, int& b, int wm, int wn,
                                             int lane, bf16x8 (&fa)[WM / 32], typename BFrag<F8>::raw (&fb)[WN / 32],
@@ -723,8 +695,8 @@ __device__ __forceinline__ void tile_stages(const i32x4& ra, const LoadSrc<A_INS
 
 // tile_stages for the M16 path (stage16 per stage).
 template <int BM, int BN, int WM, int WN, int A_INS, int B_INS, int RG, bool SW>
-__device__ __forceinline__ void tile_stages16(const i32x4& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
-                                              const i32x4& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
+__device__ __forceinline__ void tile_stages16(const Rsrc& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
+                                              const Rsrc& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
                                               uint32_t Kbytes, int KB, int wv, uint32_t lane16,
                                               Ring<BM, BN, false, false>& ring, uint32_t ring0, int& b, int wm,
                                               int wn, int lane, bf16x8 (&fa)[WM / 16], bf16x8 (&fb)[WN / 16],
@@ -756,8 +728,8 @@ __device__ __forceinline__ void tile_stages16(const i32x4& ra, const LoadSrc<A_I
 
 // tile_stages for Q8 (same stream, stage_q8 per stage).
 template <int BM, int BN, int WM, int WN, int A_INS, int B_INS, int RG>
-__device__ __forceinline__ void tile_stages_q8(const i32x4& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
-                                               const i32x4& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
+__device__ __forceinline__ void tile_stages_q8(const Rsrc& ra, const LoadSrc<A_INS>& cs, int nkt, bool has_nxt,
+                                               const Rsrc& nrb, int nkt0, const uint32_t (&cpart)[A_INS],
                                                uint32_t Kbytes, int KB, int wv, uint32_t lane16,
                                                Ring<BM, BN, false, false>& ring, uint32_t ring0, int& b, int wm,
                                                int wn, int lane, v8i (&fa)[2], v8i (&fb)[WN / 32],
@@ -898,7 +870,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
         cpart[i] = (uint32_t)swz(slot[i], lane % 4) * 16u;
     }
     const uint32_t a_rows = GATE_UP ? (uint32_t)(g.A_max / g.k) : (uint32_t)g.A_max;
-    const i32x4 ra = make_rsrc(g.a, a_rows * Kbytes);
+    const Rsrc ra = buffer_rsrc(g.a, a_rows * Kbytes);
     const uint32_t lane16 = (uint32_t)lane * 16u;
 
     Tile cur = decode<BM, SM>(tt, t0, NT, S, g.group_n, KT);
@@ -911,7 +883,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     const int t1 = tile_index(L + GRID, total, xm);
     bool has_nxt = t1 >= 0;
     Tile nxt = cur;
-    i32x4 nrb = cs.rb;
+    Rsrc nrb = cs.rb;
     uint32_t held[A_INS];
 #pragma unroll
     for (int i = 0; i < A_INS; ++i)
@@ -989,7 +961,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     // Prologue: the first kAhead stages of the stream (all of the first tile,
     // which has at least kAhead stages), then the k step 0 fragments of the
     // first one.
-    const uint32_t ring0 = lds_addr(&ring);
+    const uint32_t ring0 = lds_address(&ring);
     constexpr uint32_t kStageBytes = sizeof(Stage<BM, BN, F8>);
 #pragma unroll
     for (int p = 0; p < kAhead; ++p) {
@@ -1071,7 +1043,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
         const int t2 = has_nxt ? tile_index(L + 2 * GRID, total, xm) : -1;
         const bool has_nn = t2 >= 0;
         Tile nn = nxt;
-        i32x4 nnrb = nrb;
+        Rsrc nnrb = nrb;
         uint32_t nheld[A_INS];
 #pragma unroll
         for (int i = 0; i < A_INS; ++i)
@@ -1428,7 +1400,7 @@ __device__ __forceinline__ int swz64(int r, int c)
 }
 
 struct Src64 {
-    i32x4 rb;          // weight panel
+    Rsrc rb;          // weight panel
     uint32_t aoff[8];  // per A load: row byte offset + this lane's chunk
     int kt;            // 64-wide stage index along K
 };
@@ -1436,7 +1408,7 @@ struct Src64 {
 // Load q (0..15) of this wave's share of a stage at LDS byte address lds:
 // q < 8: tile rows (wv*8 + q)*8 .. +8, 128 bytes each; q >= 8: weight block
 // wv*8 + q - 8 (32-row block /4, 16-k block %4).
-__device__ __forceinline__ void issue64(int q, const i32x4& ra, const Src64& ls, int KB, int wv, uint32_t lane16,
+__device__ __forceinline__ void issue64(int q, const Rsrc& ra, const Src64& ls, int KB, int wv, uint32_t lane16,
                                         uint32_t lds)
 {
     if (q < 8) {
@@ -1467,7 +1439,7 @@ struct Frag64 {
 };
 
 template <int RG, bool SW>
-__device__ __forceinline__ void stage64(const i32x4& ra, const Src64& ls, uint32_t ld_lds, int KB, int wv,
+__device__ __forceinline__ void stage64(const Rsrc& ra, const Src64& ls, uint32_t ld_lds, int KB, int wv,
                                         uint32_t lane16, const Stage64* st, const Stage64* st_next, int wm, int wn,
                                         int lane, bf16x8 (&fa)[8], bf16x8 (&fb)[8], Acc4 (&acc)[4][4])
 {
@@ -1527,8 +1499,8 @@ __device__ __forceinline__ void stage64(const i32x4& ra, const Src64& ls, uint32
 // and loads stream stage j + 2 (this tile's, the next tile's first two, or,
 // past the last tile, a reload of this tile's last stage that nobody reads).
 template <int RG, bool SW>
-__device__ __forceinline__ void tile_stages64(const i32x4& ra, const Src64& cs, int nkt, bool has_nxt,
-                                              const i32x4& nrb, int nkt0, const uint32_t (&cpart)[2],
+__device__ __forceinline__ void tile_stages64(const Rsrc& ra, const Src64& cs, int nkt, bool has_nxt,
+                                              const Rsrc& nrb, int nkt0, const uint32_t (&cpart)[2],
                                               uint32_t Kbytes, int KB, int wv, uint32_t lane16, Ring64& ring,
                                               uint32_t ring0, int& b, int wm, int wn, int lane, bf16x8 (&fa)[8],
                                               bf16x8 (&fb)[8], const uint32_t (&held)[8], Acc4 (&acc)[4][4])
@@ -1596,7 +1568,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     for (int p = 0; p < 2; ++p)
         cpart[p] = (uint32_t)swz64(slot[p], lane & 7) * 16u;
     const uint32_t a_rows = GATE_UP ? (uint32_t)(g.A_max / g.k) : (uint32_t)g.A_max;
-    const i32x4 ra = make_rsrc(g.a, a_rows * Kbytes);
+    const Rsrc ra = buffer_rsrc(g.a, a_rows * Kbytes);
     const uint32_t lane16 = (uint32_t)lane * 16u;
 
     Tile cur = decode<BM, SM>(tt, t0, NT, S, g.group_n, KT);
@@ -1609,7 +1581,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     const int t1 = tile_index(L + GRID, total, xm);
     bool has_nxt = t1 >= 0;
     Tile nxt = cur;
-    i32x4 nrb = cs.rb;
+    Rsrc nrb = cs.rb;
     uint32_t held[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -1639,7 +1611,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 
     // Prologue: stream stages 0 and 1 (the first tile has at least 2), then
     // stage 0's k-step 0 fragments.
-    const uint32_t ring0 = lds_addr(&ring);
+    const uint32_t ring0 = lds_address(&ring);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         Src64 ls = cs;
@@ -1684,7 +1656,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
         const int t2 = has_nxt ? tile_index(L + 2 * GRID, total, xm) : -1;
         const bool has_nn = t2 >= 0;
         Tile nn = nxt;
-        i32x4 nnrb = nrb;
+        Rsrc nnrb = nrb;
         uint32_t nheld[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)

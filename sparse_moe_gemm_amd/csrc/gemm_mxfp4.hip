@@ -50,11 +50,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr int kBN = 256;  // weight rows per tile
 
-__device__ __forceinline__ float silu_fast(float z)
-{
-    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-}
-
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b)
 {
     return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
@@ -394,7 +389,7 @@ __global__ __launch_bounds__(WAVES_M * 4 * kWave)
                     float h[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        h[q] = silu_fast(acc[0][i][4 * q4 + q]) * acc[1][i][4 * q4 + q];
+                        h[q] = silu_rcp(acc[0][i][4 * q4 + q]) * acc[1][i][4 * q4 + q];
                     *(uint2*)(hp + 8 * q4) = make_uint2(bf16x2_bits(h[0], h[1]), bf16x2_bits(h[2], h[3]));
                 }
             } else {

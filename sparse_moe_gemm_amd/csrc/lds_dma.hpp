@@ -1,4 +1,5 @@
-// lds_dma.hpp - direct buffer->LDS loads of gfx950 for the 4-bit weight GEMMs.
+// lds_dma.hpp - buffer resources and direct buffer->LDS loads of gfx950 for the
+// grouped GEMMs.
 #pragma once
 
 #include "common.hpp"
@@ -7,7 +8,8 @@ namespace cmoe {
 
 typedef int32_t Rsrc __attribute__((ext_vector_type(4)));
 
-// Resource of a raw byte buffer (loads past `bytes` give zeros).
+// Resource of a raw byte buffer: base address, size in bytes (loads past it give
+// zeros instead of touching memory), stride 0.
 __device__ __forceinline__ Rsrc buffer_rsrc(const void* base, uint32_t bytes)
 {
     const uint64_t a = (uint64_t)(uintptr_t)base;
