@@ -28,15 +28,19 @@
 //   * h is kept as a pair of bf16 (value and remainder, 16 significant bits):
 //     the second MFMA it costs is free here, and h adds no error to speak of.
 //   * Weights are read with non-temporal loads, two register sets in flight.
-// Measured (GPU time of the two kernels): 1 token, bf16, 8 experts of 4096 x
-// 14336, k = 2: 77 + 41 us for 470 + 235 MB (6.1 and 5.8 TB/s; a plain read of
-// memory reaches 5.7 - 6.2); 16 tokens, bf16, 128 of 2048 x 768, k = 4: 69 + 31 us
-// for about 320 + 160 MB, 9 us of it the routing's 512 KB per workgroup; 7 tokens,
-// 4-bit, 8 x 4096 x 14336: 73 + 41 us for 433 + 216 MB; 3 tokens, 8-bit, 64 x 4096
-// x 1408: 19 + 11 us for 28 + 14 MB, bound by latency (start, routing, two
-// reductions). A very small layer takes 8 + 4 us. Reading the down weights ahead
-// into the caches at the end of the first kernel cost 1 - 5 us instead of saving
-// any.
+// Measured (GPU time of the two kernels, bytes of the experts that were active):
+// 1 token, bf16, 8 experts of 4096 x 14336, k = 2: 77 + 41 us for 470 + 235 MB
+// (6.1 and 5.8 TB/s; a plain read of memory reaches 5.7 - 6.2); 16 tokens, bf16,
+// 128 of 2048 x 768, k = 4, 50 active: 69 + 31 us for 315 + 157 MB, 9 us of it the
+// routing's 512 KB per workgroup; 7 tokens, 4-bit, 8 of 4096 x 14336, 6 active: 73
+// + 41 us for 374 + 187 MB (5.1 and 4.5 TB/s); 3 tokens, 8-bit, 64 of 4096 x 1408:
+// 19 + 11 us for 29 + 14 MB, bound by latency (start, routing, two reductions). A
+// very small layer takes 8 + 4 us. Against the general path (whole calls, us, 1 / 7
+// / 16 tokens, 8 experts of 4096 x 14336): bf16 122 / 320 / 438 and 170 / 364 /
+// 440, 8-bit 72 / 184 / 251 and 109 / 212 / 250, 4-bit 52 / 115 / 158 and 67 / 133
+// / 155: 16 tokens on few large experts gain nothing. Reading the down weights
+// ahead into the caches at the end of the first kernel cost 1 - 5 us instead of
+// saving any.
 #include "mxfp4.hpp"
 #include "topk.hpp"
 

@@ -20,9 +20,11 @@
 // persistent workgroup walks its tiles (tiles.hpp) and streams their K stages
 // (64 k of bf16 rows, 128 k of 4-bit rows) through a ring of SLOTS LDS slots:
 // while stage s is multiplied, the next SLOTS - 1 are on their way, across tile
-// borders too. One wait and one barrier per stage: after it every wave's loads
-// of stage s are in LDS and every wave has read stage s - 1 to the end, so its
-// slot can take stage s + SLOTS - 1. Weights are streamed straight into LDS in
+// borders too, but for gate/up on bf16 rows: its next tile's row numbers come
+// from perm when they are needed, and as vector memory returns in order, the
+// wait for them is a wait for all stages in flight. One wait and one barrier per
+// stage: after it every wave's loads of stage s are in LDS and every wave has
+// read stage s - 1 to the end, so its slot can take stage s + SLOTS - 1. Weights are streamed straight into LDS in
 // whole 1 KiB blocks, which keeps enough of them in flight to read HBM at 5.1 -
 // 5.4 TB/s from experts of a few rows (32 tokens on 8 experts of 4096 x 14336:
 // gate/up 499 MB in 90 us, down 249 MB in 47 us; streaming them into registers
@@ -422,6 +424,9 @@ hipError_t launch_shape(const MxGemmArgs& a, hipStream_t s)
 }
 
 // Rows per tile from the mean rows per expert (the routing is on the device).
+// The choice would be better for the number of tiles as well: few large experts
+// (112 n-tiles each) still gain by tiles of 64 rows at 64 rows on average, where
+// many small ones lose, and the rule takes 128 for both.
 // A tile costs its weights' stages whatever rows it holds, and its multiplied
 // row groups; an expert with a few rows more than the tile pays for two.
 // Gate/up + down in us with tiles of 64 / 128 rows, bf16 rows: 8 experts of

@@ -39,8 +39,8 @@ __device__ __forceinline__ float mx_inv_scale(uint32_t b)
 
 // Eight codes of v[0..7] * inv, value i in bits 4i .. 4i+3: nearest E2M1 value,
 // ties to the even mantissa, the sign kept by zeros. v_cvt_scalef32_pk_fp4_f32
-// rounds so on every f32 of magnitude at most 6 (compared with a model of the
-// rule on all of them), and the products are exact wherever they are not far
+// rounds so on every f32 of magnitude at most 6 (a test compares all of them with
+// the rule), and the products are exact wherever they are not far
 // below the smallest code.
 __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], float inv)
 {
