@@ -163,24 +163,27 @@ def _on_device_of(t, fn, *args):
 
 
 def _check_stream(stream, device):
-    if stream is not None and stream.device != device:
+    if stream.device != device:
         raise ValueError("the stream belongs to another device than the tensor")
 
 
-def _new_output(shape, dtype, device, stream):
-    """An output of a call on `stream` (None: the current one). It is memory of
-    that stream's own pool: what the allocator hands out of the current
-    stream's pool may still be in use by kernels queued there, which nothing
-    orders before `stream`. The current stream is recorded as a user, since
-    the caller goes on there."""
+def _empty_on(stream, device):
+    """torch.empty for the outputs of a call on a given stream of `device`. Their
+    memory is of that stream's own pool: what the allocator hands out of the
+    current stream's pool may still be in use by kernels queued there, which
+    nothing orders before `stream`. The current stream is recorded as a user,
+    since the caller goes on there."""
     import torch
 
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
+    _check_stream(stream, device)
+
+    def empty(shape, dtype):
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream(device))
+        return t
+
+    return empty
 
 
 def quantize_fp8(w, stream=None):
@@ -194,9 +197,12 @@ def quantize_fp8(w, stream=None):
     if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_cuda or not w.is_contiguous():
         raise TypeError("w must be a contiguous 2-D bfloat16 device tensor")
     rows, cols = w.shape
-    _check_stream(stream, w.device)
-    codes = _new_output((rows, cols), torch.uint8, w.device, stream)
-    scales = _new_output((rows,), torch.float32, w.device, stream)
+    if stream is None:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((rows,), dtype=torch.float32, device=w.device)
+    else:
+        empty = _empty_on(stream, w.device)
+        codes, scales = empty((rows, cols), torch.uint8), empty((rows,), torch.float32)
     st = _on_device_of(w, colibri_moe_quantize_fp8, w.data_ptr(), rows, cols, codes.data_ptr(), scales.data_ptr(),
                        _stream_of(w, stream))
     if stream is not None:
@@ -232,9 +238,12 @@ def quantize_mxfp4(w, stream=None):
     row_stride, step = w.stride()
     if cols % 32 != 0 or (cols > 1 and step != 1) or (rows > 1 and row_stride < cols):
         raise ValueError("rows must be contiguous, a multiple of 32 long, and must not overlap")
-    _check_stream(stream, w.device)
-    codes = _new_output((rows, cols // 2), torch.uint8, w.device, stream)
-    scales = _new_output((rows, cols // 32), torch.uint8, w.device, stream)
+    if stream is None:
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=w.device)
+    else:
+        empty = _empty_on(stream, w.device)
+        codes, scales = empty((rows, cols // 2), torch.uint8), empty((rows, cols // 32), torch.uint8)
     if rows == 0 or cols == 0:
         return codes, scales
     st = _on_device_of(w, colibri_moe_quantize_mxfp4, w.data_ptr(), BF16 if bf16 else F32, rows, cols,
@@ -263,8 +272,11 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     rows, cols = codes.shape[0], codes.shape[1] * 2
     if scales.device != codes.device or scales.shape[0] != rows or scales.shape[1] * 32 != cols:
         raise ValueError("codes [rows][cols/2] and scales [rows][cols/32] do not belong together")
-    _check_stream(stream, codes.device)
-    out = _new_output((rows, cols), torch.bfloat16 if bf16 else torch.float32, codes.device, stream)
+    value = torch.bfloat16 if bf16 else torch.float32
+    if stream is None:
+        out = torch.empty((rows, cols), dtype=value, device=codes.device)
+    else:
+        out = _empty_on(stream, codes.device)((rows, cols), value)
     if rows == 0 or cols == 0:
         return out
     st = _on_device_of(codes, colibri_moe_dequantize_mxfp4, codes.data_ptr(), scales.data_ptr(), rows, cols,
@@ -341,7 +353,8 @@ class MoELayer:
         wts = Weights(w_router.data_ptr(), None if b_router is None else b_router.data_ptr(),
                       w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr())
         self.device = w_router.device
-        _check_stream(stream, self.device)
+        if stream is not None:
+            _check_stream(stream, self.device)
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
         st, h = _on_device_of(w_router, colibri_moe_init, self.cfg, wts, self.stream.cuda_stream)
         if st != OK:
@@ -390,7 +403,7 @@ class MoELayer:
         other = torch._C._cuda_getCurrentRawStream(x.device.index) != self.stream.cuda_stream
         given = y
         if y is None:
-            y = _new_output(x.shape, x.dtype, x.device, self.stream if other else None)
+            y = _empty_on(self.stream, x.device)(x.shape, x.dtype) if other else torch.empty_like(x)
         if other:
             for t in (x, given, *((routing or {}).get(n) for n, _ in Routing._fields_)):
                 if t is not None:

@@ -12,9 +12,11 @@ from test_gpu_mxfp4 import CASES as LAYERS
 
 C = synth.LayerConfig
 # Long rows of W_down: the few-token down kernel takes several trips through its
-# two register sets (all modes), with a last partial one.
+# two register sets (all modes), with a last partial one. Long token rows: three
+# chunks of the token fragments that the gate/up kernel keeps.
 FEW_DEEP = [C("deep-3", 3, 256, 8, 4, 8448, "bf16"), C("deep-16", 16, 256, 8, 4, 8448, "bf16"),
-            C("deep-9", 9, 384, 4, 2, 4352, "bf16")]
+            C("deep-9", 9, 384, 4, 2, 4352, "bf16"), C("chunks-6", 6, 8448, 3, 2, 256, "bf16"),
+            C("chunks-16", 16, 8576, 3, 1, 384, "bf16")]
 # Down GEMMs of the 4-bit layers in two and four K splits, from even and odd K
 # units, for one m-tile of every height and for many.
 LAYERS_DEEP = [
