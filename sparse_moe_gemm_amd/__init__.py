@@ -397,6 +397,8 @@ class MoELayer:
         if y is not None and (y.dtype != self.dtype or not y.is_contiguous() or y.device != self.device
                               or y.numel() < T * self.d):
             raise TypeError("y must be a contiguous [T][d] tensor of the layer dtype on the layer's device")
+        if routing is not None:
+            self._check_routing(routing, T)
         # The kernels run on the handle's stream: when that is not the current
         # one, a y made here is memory of its pool, and the memory of the
         # caller's tensors is not used again before it is done with them.
@@ -410,7 +412,6 @@ class MoELayer:
                     t.record_stream(self.stream)
         r = None
         if routing is not None:
-            self._check_routing(routing, T)
             r = Routing(*[routing[n].data_ptr() if routing.get(n) is not None else None
                           for n, _ in Routing._fields_])
         st = fn(self.handle, x.data_ptr(), T, y.data_ptr(), r)

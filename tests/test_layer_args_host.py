@@ -119,3 +119,12 @@ def test_layer_lives_on_its_weights_device(dev, monkeypatch):
     with pytest.raises(ValueError):
         cm.MoELayer(**weights(dev, index=1), top_k=2, max_tokens=16, stream=fake_device.Stream(0x62))
     assert len(made) == 2
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_a_refused_call_on_another_stream_leaves_its_tensors_alone(dev, calls, entry):
+    layer = fake_device.layer(dev, stream=fake_device.Stream(0x63))
+    x, ids = tensor(dev, (4, 64), BF16), tensor(dev, (4, 2), I32)
+    with pytest.raises(TypeError, match="inv"):
+        getattr(layer, entry)(x, None, {"topk_ids": ids, "inv": torch.zeros(8, dtype=I32)})
+    assert not calls and not dev.made and not x.recorded and not ids.recorded
