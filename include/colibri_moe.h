@@ -170,6 +170,43 @@ typedef struct colibri_moe colibri_moe_t; /* opaque handle */
 colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_config_t* cfg,
                                       const colibri_moe_weights_t* w, void* hip_stream);
 
+/* How a token's experts are chosen and weighted, for layers whose model does
+ * not take the softmax over the k largest logits. The pages' two-level expert
+ * topologies («Colibri 是什么» (nxbn.cn) §2.3) choose groups of experts first:
+ *
+ *   s_e  = sigmoid(l_e), or the softmax of l over all E experts
+ *   c_e  = s_e + bias_e                    (bias: for the choice alone, may be absent)
+ *   the top_groups of the n_groups groups of E / n_groups consecutive experts
+ *   with the largest score stay: their largest c, or the sum of their two largest
+ *   ids  = the k largest c among them, slot 0 = largest
+ *   w_j  = scale * s_ids[j] / sum_j' s_ids[j'], without the division if not normalize
+ *
+ * Ties go to the lower index, for groups as for experts. fp32 throughout. An
+ * expert whose logit is -inf or NaN (or whose c is) is out: it is chosen only
+ * when the groups that stay hold fewer than k others, behind them, with weight
+ * 0; a group's score counts the others alone, and is -inf if there are none.
+ * Where the weights of all k are 0 they stay 0. Equal infinite logits share
+ * the softmax. */
+typedef enum { COLIBRI_MOE_SCORE_SOFTMAX = 0, COLIBRI_MOE_SCORE_SIGMOID = 1 } colibri_moe_scoring_t;
+typedef enum { COLIBRI_MOE_GROUP_MAX = 0, COLIBRI_MOE_GROUP_TOP2 = 1 } colibri_moe_group_score_t;
+typedef struct {
+    colibri_moe_scoring_t scoring;
+    int32_t n_groups;    /* divides E, at most 64; 1: no groups */
+    int32_t top_groups;  /* 1..n_groups, their experts at least k */
+    colibri_moe_group_score_t group_score;
+    int32_t normalize;   /* 0 or 1 */
+    float scale;         /* finite */
+} colibri_moe_rule_t;
+
+/* colibri_moe_init for a layer that routes by a rule: every forward of the
+ * handle (also forward_static and forward_few, whose router then runs as a
+ * launch of its own) chooses and weights its experts so; all else is the same.
+ * bias: [E] fp32 on the device, 4-byte aligned, copied; NULL for none. A rule
+ * that does not fit the layer is INVALID_ARG. */
+colibri_moe_status_t colibri_moe_init_rule(colibri_moe_t** out, const colibri_moe_config_t* cfg,
+                                           const colibri_moe_weights_t* w, const colibri_moe_rule_t* rule,
+                                           const float* bias, void* hip_stream);
+
 /* y [T][d_model] = MoE layer of x [T][d_model]. T = 0 returns OK and does
  * nothing. routing_out may be NULL. Allocates nothing. */
 colibri_moe_status_t colibri_moe_forward(colibri_moe_t* h, const void* x, int32_t T, void* y,
@@ -248,6 +285,51 @@ colibri_moe_status_t colibri_moe_quantize_mxfp4(const void* w, colibri_moe_dtype
  * this format are given to init so. */
 colibri_moe_status_t colibri_moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                                   int64_t cols, colibri_moe_dtype_t dtype, void* out, void* hip_stream);
+
+/* The same choice for given logits [T][E] (fp32 or bf16, row t starting at
+ * element t * row_stride, aligned to their type): ids and weights [T][k], 4-byte
+ * aligned. E <= 256, k <= min(8, E), row_stride >= E, T >= 0 (0: nothing to do),
+ * T * row_stride <= 2^42; INVALID_ARG otherwise, UNSUPPORTED for more experts or
+ * a larger k. bias as for colibri_moe_init_rule. Caller-owned DEVICE buffers.
+ * Enqueues on hip_stream (NULL = default stream) and returns without waiting.
+ * Needs no handle. */
+colibri_moe_status_t colibri_moe_route(const void* logits, colibri_moe_dtype_t dtype, int64_t row_stride, int32_t T,
+                                       int32_t E, int32_t k, const colibri_moe_rule_t* rule, const float* bias,
+                                       int32_t* ids, float* weights, void* hip_stream);
+
+/* Root-mean-square norm of rows, the step in front of a layer, with the
+ * residual's addition and 8-bit rows for products that take them:
+ *   v = x + residual (fp32),  residual_out = v,  y = v / sqrt(mean(v^2) + eps) * weight,
+ *   codes, scales: E4M3 rows of y by the rule above (one power of two a row),
+ * each output rounded once from fp32; the mean is taken in 64 bits. A code of
+ * an infinity or NaN is NaN, and the row's scale is the other values'.
+ * rows x cols values; row t of x, residual and residual_out starts at element
+ * t * their stride (at least cols); y, codes [rows][cols] and scales [rows] are
+ * dense. residual, residual_out, y and codes (with scales) may be NULL, but not
+ * all outputs. residual_out may be residual and y may be x (with the same
+ * stride); other overlaps are not allowed. Pointers aligned to their type
+ * (ALIGNMENT); rows >= 0 (0: nothing to do), 1 <= cols <= 2^24, rows * stride <=
+ * 2^42, eps > 0, finite; INVALID_ARG otherwise. Caller-owned DEVICE buffers.
+ * Enqueues on hip_stream (NULL = default stream) and returns without waiting.
+ * Needs no handle. */
+typedef struct {
+    const void* x;
+    int64_t x_stride;
+    const void* residual;
+    int64_t residual_stride;
+    const void* weight;                /* [cols] */
+    colibri_moe_dtype_t dtype;         /* of x, residual, y and residual_out */
+    colibri_moe_dtype_t weight_dtype;
+    int64_t rows;
+    int32_t cols;
+    float eps;
+    void* y;
+    void* residual_out;
+    int64_t residual_out_stride;
+    uint8_t* codes;
+    float* scales;
+} colibri_moe_norm_t;
+colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip_stream);
 
 /* Measurement helper, not a step of the layer: copies `bytes` bytes from src
  * to dst (caller-owned DEVICE buffers, 16-byte aligned, not overlapping;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libcolibri_moe.so")
@@ -44,11 +45,24 @@ class Routing(ctypes.Structure):
                 ("perm", ctypes.c_void_p), ("perm_slot", ctypes.c_void_p), ("inv", ctypes.c_void_p)]
 
 
-EXPORTS = ("colibri_moe_init", "colibri_moe_forward", "colibri_moe_forward_static",
+class Rule(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int), ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("rows", ctypes.c_int64), ("cols", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("y", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+EXPORTS = ("colibri_moe_init", "colibri_moe_init_rule", "colibri_moe_forward", "colibri_moe_forward_static",
            "colibri_moe_forward_few", "colibri_moe_free",
            "colibri_moe_status_string", "colibri_moe_stage_times", "colibri_moe_stage_name",
            "colibri_moe_quantize_fp8", "colibri_moe_quantize_mxfp4", "colibri_moe_dequantize_mxfp4",
-           "colibri_moe_stream_copy")
+           "colibri_moe_route", "colibri_moe_rms_norm", "colibri_moe_stream_copy")
 
 _lib = None
 
@@ -64,6 +78,9 @@ def lib() -> ctypes.CDLL:
         P, i32 = ctypes.c_void_p, ctypes.c_int32
         L.colibri_moe_init.restype = ctypes.c_int
         L.colibri_moe_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(Config), ctypes.POINTER(Weights), P]
+        L.colibri_moe_init_rule.restype = ctypes.c_int
+        L.colibri_moe_init_rule.argtypes = [ctypes.POINTER(P), ctypes.POINTER(Config), ctypes.POINTER(Weights),
+                                            ctypes.POINTER(Rule), P, P]
         L.colibri_moe_forward.restype = ctypes.c_int
         L.colibri_moe_forward.argtypes = [P, P, i32, P, ctypes.POINTER(Routing)]
         L.colibri_moe_forward_static.restype = ctypes.c_int
@@ -85,6 +102,10 @@ def lib() -> ctypes.CDLL:
                                                  P]
         L.colibri_moe_dequantize_mxfp4.restype = ctypes.c_int
         L.colibri_moe_dequantize_mxfp4.argtypes = [P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P, P]
+        L.colibri_moe_route.restype = ctypes.c_int
+        L.colibri_moe_route.argtypes = [P, ctypes.c_int, ctypes.c_int64, i32, i32, i32, ctypes.POINTER(Rule), P, P, P, P]
+        L.colibri_moe_rms_norm.restype = ctypes.c_int
+        L.colibri_moe_rms_norm.argtypes = [ctypes.POINTER(Norm), P]
         L.colibri_moe_stream_copy.restype = ctypes.c_int
         L.colibri_moe_stream_copy.argtypes = [P, P, ctypes.c_int64, P]
         _lib = L
@@ -98,6 +119,14 @@ def colibri_moe_init(cfg: Config, weights: Weights, hip_stream: int = 0):
     h = ctypes.c_void_p()
     st = lib().colibri_moe_init(ctypes.byref(h), ctypes.byref(cfg), ctypes.byref(weights),
                                 ctypes.c_void_p(hip_stream))
+    return st, h.value
+
+
+def colibri_moe_init_rule(cfg: Config, weights: Weights, rule: Rule, bias_ptr, hip_stream: int = 0):
+    """Returns (status, handle)."""
+    h = ctypes.c_void_p()
+    st = lib().colibri_moe_init_rule(ctypes.byref(h), ctypes.byref(cfg), ctypes.byref(weights),
+                                     None if rule is None else ctypes.byref(rule), bias_ptr, hip_stream)
     return st, h.value
 
 
@@ -289,6 +318,162 @@ def dequantize_mxfp4(codes, scales, dtype=None, stream=None):
     return out
 
 
+class RoutingRule:
+    """How experts are chosen and weighted from logits (colibri_moe_rule_t):
+    scoring "softmax" (over all experts) or "sigmoid"; the experts in `groups`
+    equal consecutive groups, of which the `top_groups` (default: all) with the
+    largest group_score stay, "max" (their best expert) or "top2" (the sum of
+    their two best); the weights of a token divided by their sum if normalize,
+    then multiplied by scale. The default is the softmax over the k largest
+    logits."""
+
+    def __init__(self, scoring="softmax", groups=1, top_groups=None, group_score="max", normalize=True, scale=1.0):
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError('scoring must be "softmax" or "sigmoid"')
+        if group_score not in ("max", "top2"):
+            raise ValueError('group_score must be "max" or "top2"')
+        self.c = Rule(int(scoring == "sigmoid"), groups, groups if top_groups is None else top_groups,
+                      int(group_score == "top2"), int(bool(normalize)), scale)
+
+
+_default_rule = RoutingRule()
+
+
+def colibri_moe_route(logits_ptr: int, dtype: int, row_stride: int, T: int, E: int, k: int, rule: Rule, bias_ptr,
+                      ids_ptr: int, weights_ptr: int, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_route(logits_ptr, dtype, row_stride, T, E, k, None if rule is None else ctypes.byref(rule),
+                                   bias_ptr, ids_ptr, weights_ptr, hip_stream)
+
+
+def _check_select_bias(bias, E, device):
+    import torch
+
+    if bias.dtype != torch.float32 or bias.device != device or not bias.is_contiguous() or bias.numel() != E:
+        raise TypeError("the selection bias must be a contiguous float32 tensor of E values on the same device")
+
+
+def route(logits, top_k, rule: RoutingRule | None = None, bias=None, stream=None):
+    """(ids int32 [T][top_k], weights fp32 [T][top_k]) of router logits [T][E],
+    a bf16 or fp32 device tensor with contiguous rows (they may be slices of
+    longer ones), by a RoutingRule; bias [E] fp32 is added to the scores for the
+    choice alone. At most 256 experts, top_k at most 8. The work is enqueued on
+    `stream`, by default the current one; a given stream must already be
+    ordered behind the work that makes the tensors."""
+    import torch
+
+    bf16 = logits.dtype == torch.bfloat16
+    if not (bf16 or logits.dtype == torch.float32) or logits.dim() != 2 or not logits.is_cuda:
+        raise TypeError("logits must be a 2-D bfloat16 or float32 device tensor")
+    T, E = logits.shape
+    row_stride, step = logits.stride()
+    if (E > 1 and step != 1) or (T > 1 and row_stride < E):
+        raise ValueError("rows must be contiguous and must not overlap")
+    if bias is not None:
+        _check_select_bias(bias, E, logits.device)
+    if stream is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        empty = _empty_on(stream, logits.device)
+        ids, weights = empty((T, top_k), torch.int32), empty((T, top_k), torch.float32)
+        for t in (logits, bias):
+            if t is not None:
+                t.record_stream(stream)
+    st = _on_device_of(logits, colibri_moe_route, logits.data_ptr(), BF16 if bf16 else F32, row_stride if T > 1 else E,
+                       T, E, top_k, (rule or _default_rule).c, None if bias is None else bias.data_ptr(),
+                       ids.data_ptr(), weights.data_ptr(), _stream_of(logits, stream))
+    if st != OK:
+        raise ColibriError("colibri_moe_route", st)
+    return ids, weights
+
+
+def colibri_moe_rms_norm(norm: Norm, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_rms_norm(None if norm is None else ctypes.byref(norm), hip_stream)
+
+
+class Normed(NamedTuple):
+    """Outputs of rms_norm; None where a call has none."""
+
+    y: object
+    residual: object
+    codes: object
+    scales: object
+
+
+def _rows_of(t, like, name):
+    """Row stride of a 2-D device tensor that fits `like`."""
+    if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape) or t.device != like.device:
+        raise TypeError(f"{name} must have the shape, dtype and device of x")
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and stride < cols):
+        raise ValueError(f"rows of {name} must be contiguous and must not overlap")
+    return stride if rows > 1 else cols
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=None, residual_out=None, stream=None):
+    """Root-mean-square norm of the rows of x [T][d] (bf16 or fp32, rows
+    contiguous, they may be slices of longer ones) with weight [d] (x's dtype or
+    fp32), of x + residual if a residual of the same shape is given:
+    Normed(y, residual, codes, scales) with residual = x + residual. quantize
+    "fp8" also gives y's E4M3 codes (uint8) and power-of-two row scales, in
+    quantize_fp8's format, from the unrounded values; with_y=False leaves y out.
+    Given outputs y (contiguous; may be x) and residual_out (may be residual) are
+    written and returned. The work is enqueued on `stream`, by default the
+    current one; a given stream must already be ordered behind the work that
+    makes the tensors."""
+    import torch
+
+    bf16 = x.dtype == torch.bfloat16
+    if not (bf16 or x.dtype == torch.float32) or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("x must be a 2-D bfloat16 or float32 device tensor")
+    T, d = x.shape
+    x_stride = _rows_of(x, x, "x")
+    if weight.dtype not in (x.dtype, torch.float32) or weight.device != x.device or weight.dim() != 1:
+        raise TypeError("weight must be a 1-D tensor of x's dtype or float32 on x's device")
+    if weight.shape[0] != d or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous and hold d values")
+    if quantize not in (None, "fp8"):
+        raise ValueError('quantize must be None or "fp8"')
+    if y is not None and (y.dtype != x.dtype or tuple(y.shape) != (T, d) or y.device != x.device
+                          or not y.is_contiguous()):
+        raise TypeError("y must be a contiguous tensor of x's shape, dtype and device")
+    r_stride = _rows_of(residual, x, "residual") if residual is not None else d
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out without a residual")
+    ro_stride = _rows_of(residual_out, x, "residual_out") if residual_out is not None else d
+    if not with_y and y is not None:
+        raise ValueError("y given with with_y=False")
+    if not with_y and quantize is None and residual is None:
+        raise ValueError("nothing to compute")
+    if stream is None:
+        def empty(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=x.device)
+    else:
+        empty = _empty_on(stream, x.device)
+        for t in (x, weight, residual, y, residual_out):
+            if t is not None:
+                t.record_stream(stream)
+    if with_y and y is None:
+        y = empty((T, d), x.dtype)
+    if residual is not None and residual_out is None:
+        residual_out = empty((T, d), x.dtype)
+    codes = scales = None
+    if quantize is not None:
+        codes, scales = empty((T, d), torch.uint8), empty((T,), torch.float32)
+    out = Normed(y, residual_out, codes, scales)
+    if T == 0 or d == 0:
+        return out
+    dtype = BF16 if bf16 else F32
+    p = [None if t is None else t.data_ptr() for t in (residual, y, residual_out, codes, scales)]
+    n = Norm(x.data_ptr(), x_stride, p[0], r_stride, weight.data_ptr(), dtype,
+             BF16 if weight.dtype == torch.bfloat16 else F32, T, d, eps, p[1], p[2], ro_stride, p[3], p[4])
+    st = _on_device_of(x, colibri_moe_rms_norm, n, _stream_of(x, stream))
+    if st != OK:
+        raise ColibriError("colibri_moe_rms_norm", st)
+    return out
+
+
 def colibri_moe_stream_copy(src_ptr: int, dst_ptr: int, nbytes: int, hip_stream: int = 0) -> int:
     return lib().colibri_moe_stream_copy(ctypes.c_void_p(src_ptr), ctypes.c_void_p(dst_ptr), nbytes,
                                          ctypes.c_void_p(hip_stream))
@@ -325,11 +510,12 @@ class MoELayer:
     None, w_gate/w_up [E][f][d], w_down [E][d][f], all torch.bfloat16 or all
     torch.float32, on the device the layer is to run on. Its calls run on
     `stream`, by default that device's current one; a given stream must already
-    be ordered behind the work that makes the weights.
+    be ordered behind the work that makes the weights. With a rule (RoutingRule,
+    select_bias [E] fp32 or None its bias) experts are chosen and weighted by it.
     """
 
     def __init__(self, w_router, b_router, w_gate, w_up, w_down, top_k: int, max_tokens: int,
-                 flags: int = 0, stream=None):
+                 flags: int = 0, stream=None, rule: RoutingRule | None = None, select_bias=None):
         import torch
 
         self._torch = torch
@@ -356,9 +542,17 @@ class MoELayer:
         if stream is not None:
             _check_stream(stream, self.device)
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        st, h = _on_device_of(w_router, colibri_moe_init, self.cfg, wts, self.stream.cuda_stream)
+        if select_bias is not None:
+            if rule is None:
+                raise ValueError("select_bias without a rule")
+            _check_select_bias(select_bias, E, self.device)
+        if rule is None:
+            st, h = _on_device_of(w_router, colibri_moe_init, self.cfg, wts, self.stream.cuda_stream)
+        else:
+            st, h = _on_device_of(w_router, colibri_moe_init_rule, self.cfg, wts, rule.c,
+                                  None if select_bias is None else select_bias.data_ptr(), self.stream.cuda_stream)
         if st != OK:
-            raise ColibriError("colibri_moe_init", st)
+            raise ColibriError("colibri_moe_init" if rule is None else "colibri_moe_init_rule", st)
         self.handle = h
 
     def routing_buffers(self, T: int) -> dict:

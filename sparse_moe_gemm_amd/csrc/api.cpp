@@ -9,6 +9,7 @@
 // enqueues kernels.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <algorithm>
 #include <mutex>
@@ -78,6 +79,7 @@ struct colibri_moe {
     int few_split;      // parts of its down kernel's sums,
     float* few_part;    // their sums [few_split][16][d]
     int32_t* few_count; // and arrivals per column block (at most [d/32]), zero between calls
+    SelectRule rule;    // how experts are chosen (its bias in the arena)
     int32_t* ccnt;  // fused combine: arrivals per token and 128-column tile [max_tokens][d/128], zero between calls
     bool timing;
     hipEvent_t ev[kStages + 1];
@@ -227,6 +229,24 @@ colibri_moe_status_t validate_config(const colibri_moe_config_t* c)
     return COLIBRI_MOE_OK;
 }
 
+colibri_moe_status_t check_rule(const colibri_moe_rule_t* r, int E, int k)
+{
+    if ((r->scoring != COLIBRI_MOE_SCORE_SOFTMAX && r->scoring != COLIBRI_MOE_SCORE_SIGMOID) ||
+        (r->group_score != COLIBRI_MOE_GROUP_MAX && r->group_score != COLIBRI_MOE_GROUP_TOP2) ||
+        (r->normalize != 0 && r->normalize != 1) || !std::isfinite(r->scale))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (r->n_groups < 1 || r->n_groups > 64 || E % r->n_groups != 0 || r->top_groups < 1 ||
+        r->top_groups > r->n_groups || r->top_groups * (E / r->n_groups) < k)
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    return COLIBRI_MOE_OK;
+}
+
+SelectRule select_rule(const colibri_moe_rule_t* r, const float* bias)
+{
+    return SelectRule{1, r->scoring == COLIBRI_MOE_SCORE_SIGMOID, r->n_groups, r->top_groups,
+                      r->group_score == COLIBRI_MOE_GROUP_TOP2, r->normalize, r->scale, bias};
+}
+
 #define CMOE_HIP(call)                      \
     do {                                    \
         if ((call) != hipSuccess)           \
@@ -302,7 +322,7 @@ size_t layout_workspace(const colibri_moe* h, int64_t T, bool up_to, uint8_t* ba
     return cv.off;
 }
 
-colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
+colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w, const float* select_bias)
 {
     const colibri_moe_config_t& c = h->cfg;
     const size_t es = (size_t)h->esize;
@@ -311,6 +331,7 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     Carver cv;
     const size_t o_wrt = cv.take(router_weight_bytes((int)d, (int)E, (int)es));
     const size_t o_br = cv.take(E * sizeof(float));
+    const size_t o_sb = select_bias ? cv.take(E * sizeof(float)) : 0;
     const size_t wes = h->fp8 ? 1 : es;  // bytes per stored expert weight (mx4: below)
     const size_t o_wgu = cv.take(h->mx4 ? mx_weight_bytes(E, 2 * f, d) : E * 2 * f * d * wes);
     const size_t o_wd = cv.take(h->mx4 ? mx_weight_bytes(E, d, f) : E * d * f * wes);
@@ -336,6 +357,7 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     uint8_t* base = (uint8_t*)h->arena;
     h->w_rt = base + o_wrt;
     h->b_r = (float*)(base + o_br);
+    h->rule.bias = select_bias ? (float*)(base + o_sb) : nullptr;
     h->w_gu = base + o_wgu;
     h->w_d = base + o_wd;
     h->s_gu = h->fp8 ? (float*)(base + o_sgu) : nullptr;
@@ -358,6 +380,8 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
         CMOE_HIP(hipMemcpyAsync(h->b_r, w->b_router, E * sizeof(float), hipMemcpyDeviceToDevice, s));
     else
         CMOE_HIP(hipMemsetAsync(h->b_r, 0, E * sizeof(float), s));
+    if (select_bias)
+        CMOE_HIP(hipMemcpyAsync(base + o_sb, select_bias, E * sizeof(float), hipMemcpyDeviceToDevice, s));
     if (h->fp8) {
         // row scales, then E4M3 codes in the fp8 blocked layout (gate/up
         // interleaved by 32 rows, scales in the interleaved row order)
@@ -384,12 +408,9 @@ colibri_moe_status_t init_impl(colibri_moe* h, const colibri_moe_weights_t* w)
     return COLIBRI_MOE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_config_t* cfg,
-                                      const colibri_moe_weights_t* w, void* hip_stream)
+// rule null: the softmax over the k largest logits.
+colibri_moe_status_t init_handle(colibri_moe_t** out, const colibri_moe_config_t* cfg, const colibri_moe_weights_t* w,
+                                 const colibri_moe_rule_t* rule, const float* select_bias, void* hip_stream)
 {
     if (!out || !cfg || !w)
         return COLIBRI_MOE_ERR_INVALID_ARG;
@@ -400,8 +421,10 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     if (!w->w_router || !w->w_gate || !w->w_up || !w->w_down)
         return COLIBRI_MOE_ERR_INVALID_ARG;
     if (!aligned16(w->w_router) || !aligned16(w->w_gate) || !aligned16(w->w_up) || !aligned16(w->w_down) ||
-        ((uintptr_t)w->b_router & 3u))
+        ((uintptr_t)w->b_router & 3u) || ((uintptr_t)select_bias & 3u))
         return COLIBRI_MOE_ERR_ALIGNMENT;
+    if (rule && (st = check_rule(rule, cfg->n_experts, cfg->top_k)) != COLIBRI_MOE_OK)
+        return st;
 
     colibri_moe* h = new (std::nothrow) colibri_moe();
     if (!h)
@@ -409,6 +432,8 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     h->magic = kMagic;
     h->cfg = *cfg;
     h->stream = (hipStream_t)hip_stream;
+    if (rule)
+        h->rule = select_rule(rule, nullptr);
     h->esize = cfg->dtype == COLIBRI_MOE_BF16 ? 2 : 4;
     h->timing = (cfg->flags & COLIBRI_MOE_FLAG_STAGE_TIMING) != 0;
     h->fp8 = (cfg->flags & COLIBRI_MOE_FLAG_FP8_WEIGHTS) != 0;
@@ -484,7 +509,7 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
         h->dec_fuse_silu = h->dec_split_gu == 1 && env_int("CMOE_DECODE_FUSE_SILU", 1, 0, 1) != 0;
         h->dec_split_dn = cmoe::decode_split(cfg->n_experts, cfg->d_model, cfg->d_ff, kstep_dn, waves, 64);
     }
-    st = init_impl(h, w);
+    st = init_impl(h, w, select_bias);
     if (st != COLIBRI_MOE_OK) {
         release(h);
         return st;
@@ -495,6 +520,28 @@ colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_con
     }
     *out = h;
     return COLIBRI_MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+colibri_moe_status_t colibri_moe_init(colibri_moe_t** out, const colibri_moe_config_t* cfg,
+                                      const colibri_moe_weights_t* w, void* hip_stream)
+{
+    return init_handle(out, cfg, w, nullptr, nullptr, hip_stream);
+}
+
+colibri_moe_status_t colibri_moe_init_rule(colibri_moe_t** out, const colibri_moe_config_t* cfg,
+                                           const colibri_moe_weights_t* w, const colibri_moe_rule_t* rule,
+                                           const float* bias, void* hip_stream)
+{
+    if (!rule) {
+        if (out)
+            *out = nullptr;
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    }
+    return init_handle(out, cfg, w, rule, bias, hip_stream);
 }
 
 }  // extern "C"
@@ -523,7 +570,7 @@ colibri_moe_status_t forward_impl(colibri_moe* h, const void* x, int32_t T, void
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[0], s));
 
-    RouterArgs ra{x, h->w_rt, h->b_r, T, c.d_model, c.n_experts, c.top_k, ro.logits, ids, topw};
+    RouterArgs ra{x, h->w_rt, h->b_r, T, c.d_model, c.n_experts, c.top_k, ro.logits, ids, topw, h->rule};
     CMOE_HIP(bf ? launch_router_bf16(ra, s) : launch_router_f32(ra, s));
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[1], s));
@@ -734,7 +781,7 @@ colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, in
     a.m_gu = h->m_gu;
     a.m_d = h->m_d;
     a.act_quant = h->q8 || h->q4;
-    a.routed = !few_routes_itself(c.d_model, c.n_experts);
+    a.routed = h->rule.on || !few_routes_itself(c.d_model, c.n_experts);
     a.T = T;
     a.d = c.d_model;
     a.E = c.n_experts;
@@ -756,7 +803,7 @@ colibri_moe_status_t colibri_moe_forward_few(colibri_moe_t* h, const void* x, in
     if (tm)
         CMOE_HIP(hipEventRecord(h->ev[0], s));
     if (a.routed) {
-        RouterArgs ra{x, h->w_rt, h->b_r, T, c.d_model, c.n_experts, c.top_k, ro.logits, a.ids, a.w};
+        RouterArgs ra{x, h->w_rt, h->b_r, T, c.d_model, c.n_experts, c.top_k, ro.logits, a.ids, a.w, h->rule};
         CMOE_HIP(launch_router_bf16(ra, s));
     }
     if (tm) {
@@ -831,6 +878,52 @@ colibri_moe_status_t colibri_moe_dequantize_mxfp4(const uint8_t* codes, const ui
     if (((uintptr_t)codes & 3u) || !aligned16(out))
         return COLIBRI_MOE_ERR_ALIGNMENT;
     CMOE_HIP(launch_mx_dequantize(codes, scales, rows, cols, dtype == COLIBRI_MOE_BF16, out, (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_route(const void* logits, colibri_moe_dtype_t dtype, int64_t row_stride, int32_t T,
+                                       int32_t E, int32_t k, const colibri_moe_rule_t* rule, const float* bias,
+                                       int32_t* ids, float* weights, void* hip_stream)
+{
+    if (!rule || T < 0 || E < 1 || k < 1 || k > E || row_stride < E ||
+        (dtype != COLIBRI_MOE_BF16 && dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || k > kMaxTopK)
+        return COLIBRI_MOE_ERR_UNSUPPORTED;
+    const colibri_moe_status_t st = check_rule(rule, E, k);
+    if (st != COLIBRI_MOE_OK || T == 0)
+        return st;
+    if (!logits || !ids || !weights || row_stride > ((int64_t)1 << 42) / T)
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)logits & (dtype == COLIBRI_MOE_BF16 ? 1u : 3u)) || ((uintptr_t)bias & 3u) ||
+        ((uintptr_t)ids & 3u) || ((uintptr_t)weights & 3u))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    const RouteArgs a{logits, dtype == COLIBRI_MOE_BF16, row_stride, T, E, k, select_rule(rule, bias), ids, weights};
+    CMOE_HIP(launch_route(a, (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip_stream)
+{
+    if (!n || n->rows < 0 || n->cols < 1 || n->cols > 1 << 24 || !(n->eps > 0.0f) || !std::isfinite(n->eps) ||
+        (n->dtype != COLIBRI_MOE_BF16 && n->dtype != COLIBRI_MOE_F32) ||
+        (n->weight_dtype != COLIBRI_MOE_BF16 && n->weight_dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (n->rows == 0)
+        return COLIBRI_MOE_OK;
+    const auto fits = [&](int64_t stride) { return stride >= n->cols && stride <= ((int64_t)1 << 42) / n->rows; };
+    if (!n->x || !n->weight || (!n->y && !n->residual_out && !n->codes) || (n->codes && !n->scales) ||
+        !fits(n->x_stride) || (n->residual && !fits(n->residual_stride)) ||
+        (n->residual_out && !fits(n->residual_out_stride)))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    const uintptr_t mask = n->dtype == COLIBRI_MOE_BF16 ? 1u : 3u;
+    if ((((uintptr_t)n->x | (uintptr_t)n->residual | (uintptr_t)n->y | (uintptr_t)n->residual_out) & mask) ||
+        ((uintptr_t)n->weight & (n->weight_dtype == COLIBRI_MOE_BF16 ? 1u : 3u)) || ((uintptr_t)n->scales & 3u))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    const NormArgs a{n->x, n->x_stride, n->residual, n->residual_stride, n->weight, n->dtype == COLIBRI_MOE_BF16,
+                     n->weight_dtype == COLIBRI_MOE_BF16, n->rows, n->cols, n->eps, n->y, n->residual_out,
+                     n->residual_out_stride, n->codes, n->scales};
+    CMOE_HIP(launch_norm(a, (hipStream_t)hip_stream));
     return COLIBRI_MOE_OK;
 }
 

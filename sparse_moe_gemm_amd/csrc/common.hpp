@@ -79,10 +79,47 @@ __device__ __forceinline__ int max_expert_rows(const int32_t* offsets, int E)
     return __builtin_amdgcn_readfirstlane(m);
 }
 
+// Exponent e of the scale of an 8-bit row from its largest magnitude: the
+// smallest e >= -126 with amax <= 448 * 2^e, 0 for a row of zeros.
+__device__ __forceinline__ int fp8_scale_exp(float amax)
+{
+    if (!(amax > 0.f))
+        return 0;
+    int x;
+    const float f = frexpf(amax, &x);  // amax = f * 2^x, f in [0.5, 1)
+    // 448 = 0.875 * 2^9: amax <= 448 * 2^e  <=>  f * 2^(x - 9 - e) <= 0.875
+    const int e = (f <= 0.875f) ? x - 9 : x - 8;
+    return e < -126 ? -126 : e;
+}
+
 // ---------------------------------------------------------------------------
 // Host-side launchers (each defined in the .hip file of its kernel).
 // All enqueue on `s` and return the launch status.
 // ---------------------------------------------------------------------------
+
+// How experts are chosen and weighted (select.hpp).
+struct SelectRule {
+    int on;              // 0: softmax over the k largest logits (topk.hpp)
+    int sigmoid;         // scores: sigmoid, else softmax over all experts
+    int groups;          // groups of E / groups consecutive experts (at most 64),
+    int top_groups;      //   of which this many stay
+    int pair;            // a group counts by its two best choices, else by its best
+    int normalize;       // weights of a token sum to scale
+    float scale;
+    const float* bias;   // [E] added to the scores for the choice alone, or null
+};
+
+// Selection for given logits (route.hip).
+struct RouteArgs {
+    const void* logits;  // [T][E] fp32 or bf16, row t at t * ld elements
+    int bf16;
+    int64_t ld;
+    int T, E, k;
+    SelectRule rule;
+    int32_t* ids;        // [T][k]
+    float* w;            // [T][k]
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
 struct RouterArgs {
     const void* x;      // [T][d] dtype
@@ -92,6 +129,7 @@ struct RouterArgs {
     float* logits;      // [T][E] (may be NULL)
     int32_t* ids;       // [T][k]
     float* w;           // [T][k]
+    SelectRule rule;
 };
 hipError_t launch_router_bf16(const RouterArgs& a, hipStream_t s);
 hipError_t launch_router_f32(const RouterArgs& a, hipStream_t s);
@@ -219,6 +257,25 @@ hipError_t launch_act_quant(const void* x, int64_t rows, int cols, int k, const 
 // Row-major E4M3 codes of [rows][cols] bf16 with the given row scales.
 hipError_t launch_fp8_encode_rows(const void* w, const float* scales, uint8_t* codes, int64_t rows, int cols,
                                   hipStream_t s);
+
+// Root-mean-square norm of rows (norm.hip).
+struct NormArgs {
+    const void* x;        // [rows][d] bf16 or fp32, row t at t * x_ld elements
+    int64_t x_ld;
+    const void* r;        // residual, of x's type, or null
+    int64_t r_ld;
+    const void* w;        // [d] bf16 or fp32
+    int bf16, w_bf16;
+    int64_t rows;
+    int d;
+    float eps;
+    void* y;              // [rows][d] of x's type, or null
+    void* r_out;          // x + r, of x's type, or null; may be r
+    int64_t r_out_ld;
+    uint8_t* codes;       // [rows][d] E4M3, or null
+    float* scales;        // [rows], with codes
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 
 // 4-bit microscaled rows and weights (quant_mxfp4.hip; format and GEMM layout
 // in mxfp4.hpp). Codes [rows][cols/2] and scale bytes [rows][cols/32] of bf16

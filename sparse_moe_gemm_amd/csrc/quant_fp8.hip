@@ -30,18 +30,6 @@ namespace cmoe {
 
 namespace {
 
-// Exponent e of the row scale from the row's largest magnitude.
-__device__ __forceinline__ int fp8_scale_exp(float amax)
-{
-    if (!(amax > 0.f))
-        return 0;
-    int x;
-    const float f = frexpf(amax, &x);  // amax = f * 2^x, f in [0.5, 1)
-    // 448 = 0.875 * 2^9: amax <= 448 * 2^e  <=>  f * 2^(x - 9 - e) <= 0.875
-    const int e = (f <= 0.875f) ? x - 9 : x - 8;
-    return e < -126 ? -126 : e;
-}
-
 // Per-row scales. One wave per row of `cols` bf16 values (cols % 8 == 0);
 // with `two_src`, combined row n of a [E][2f] matrix comes from w0 (gate) when
 // n % 64 < 32, else from w1 (up), source row (n/64)*32 + n%32 of expert e.

@@ -20,7 +20,7 @@
 // partial sums through LDS in a fixed order, so results are bit-reproducible
 // and do not depend on the number of tokens in the call.
 // fp32 path: plain FMA dot products (gfx950 has no faster fp32 matrix rate).
-#include "topk.hpp"
+#include "select.hpp"
 
 namespace cmoe {
 
@@ -37,7 +37,7 @@ constexpr int kThreads = 256;  // fp32 path
 // the register budget allows: 16 waves (8 for 256 experts). A token's logits
 // do not depend on T or TG: every token is reduced by the same interleaving
 // of K over the W waves and the same LDS summation order.
-template <int NG, int TG, int W>
+template <int NG, int TG, int W, bool RULE>
 __global__ __launch_bounds__(W * kWave) void router_bf16_kernel(RouterArgs a)
 {
     constexpr int EP = 16 * NG;      // padded expert count
@@ -146,9 +146,13 @@ __global__ __launch_bounds__(W * kWave) void router_bf16_kernel(RouterArgs a)
     }
     __syncthreads();
     store_logits(&part[0][0], LDL, BT, t0, a.T, a.E, a.logits);
-    topk_softmax_epilogue<(EP + kWave - 1) / kWave>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.ids, a.w);
+    if constexpr (RULE)
+        select_epilogue<(EP + kWave - 1) / kWave>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
+    else
+        topk_softmax_epilogue<(EP + kWave - 1) / kWave>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.ids, a.w);
 }
 
+template <bool RULE>
 __global__ __launch_bounds__(kThreads) void router_f32_kernel(RouterArgs a)
 {
     __shared__ float lg[kTok][kMaxExperts + 1];
@@ -167,7 +171,10 @@ __global__ __launch_bounds__(kThreads) void router_f32_kernel(RouterArgs a)
     }
     __syncthreads();
     store_logits(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.logits);
-    topk_softmax_epilogue<kMaxExperts / kWave>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.ids, a.w);
+    if constexpr (RULE)
+        select_epilogue<kMaxExperts / kWave>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
+    else
+        topk_softmax_epilogue<kMaxExperts / kWave>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.ids, a.w);
 }
 
 __global__ void transpose_router_kernel(const uint8_t* src, uint8_t* dst, int d, int E, int esize)
@@ -211,7 +218,11 @@ hipError_t launch_router_tg(const RouterArgs& a, hipStream_t s)
 {
     constexpr int W = NG >= 16 ? 8 : 16;  // 16 waves need <= 128 registers
     const int bt = kTok * TG;
-    hipLaunchKernelGGL((router_bf16_kernel<NG, TG, W>), dim3((a.T + bt - 1) / bt), dim3(W * kWave), 0, s, a);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((a.T + bt - 1) / bt), dim3(W * kWave), 0, s, a); };
+    if (a.rule.on)
+        go(router_bf16_kernel<NG, TG, W, true>);
+    else
+        go(router_bf16_kernel<NG, TG, W, false>);
     return hipGetLastError();
 }
 
@@ -251,7 +262,11 @@ hipError_t launch_router_bf16(const RouterArgs& a, hipStream_t s)
 
 hipError_t launch_router_f32(const RouterArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL(router_f32_kernel, dim3((a.T + kTok - 1) / kTok), dim3(kThreads), 0, s, a);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((a.T + kTok - 1) / kTok), dim3(kThreads), 0, s, a); };
+    if (a.rule.on)
+        go(router_f32_kernel<true>);
+    else
+        go(router_f32_kernel<false>);
     return hipGetLastError();
 }
 
