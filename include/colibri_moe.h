@@ -103,7 +103,8 @@ typedef enum {
     COLIBRI_MOE_ERR_HIP = 5,          /* a HIP launch, copy or sync failed */
     COLIBRI_MOE_ERR_TOO_LARGE = 6     /* colibri_moe_forward_static: the call's working memory
                                          exceeds COLIBRI_MOE_STATIC_SCRATCH_BYTES;
-                                         colibri_moe_forward_few: T > COLIBRI_MOE_FEW_TOKENS */
+                                         colibri_moe_forward_few: T > COLIBRI_MOE_FEW_TOKENS;
+                                         colibri_moe_int4_linear: T*k > COLIBRI_MOE_INT4_ROWS */
 } colibri_moe_status_t;
 
 /* Size of the static working-memory array of colibri_moe_forward_static, one
@@ -113,7 +114,14 @@ typedef enum {
 /* Most tokens of a colibri_moe_forward_few call. */
 #define COLIBRI_MOE_FEW_TOKENS 16
 
-typedef enum { COLIBRI_MOE_F32 = 0, COLIBRI_MOE_BF16 = 1 } colibri_moe_dtype_t;
+/* Most rows (T * k) of a colibri_moe_int4_linear call. */
+#define COLIBRI_MOE_INT4_ROWS 128
+
+typedef enum {
+    COLIBRI_MOE_F32 = 0,
+    COLIBRI_MOE_BF16 = 1,
+    COLIBRI_MOE_F16 = 2 /* scales of 4-bit integer groups only */
+} colibri_moe_dtype_t;
 
 enum {
     COLIBRI_MOE_FLAG_ASYNC = 1u << 0,       /* forward returns after enqueueing */
@@ -330,6 +338,71 @@ typedef struct {
     float* scales;
 } colibri_moe_norm_t;
 colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip_stream);
+
+/* 4-bit integer groups, as AWQ-style checkpoints hold weights («Colibri 是什么»
+ * (nxbn.cn) names 4-bit AWQ): along a row, every `group` values share a scale s
+ * and a zero point z, and stand for (q - z) * s with codes q in 0..15. codes
+ * [rows][cols/2] (value 2i of a row in the low half of byte i), scales
+ * [rows][cols/group], zeros [rows][cols/group] bytes 0..15 (the low four bits
+ * count), or NULL: every z is 8. group: 32, 64 or a multiple of 128, dividing
+ * cols.
+ *
+ * colibri_moe_quantize_int4 makes them from w [rows][cols], bf16 or fp32, row r
+ * starting at element r * row_stride, with bf16 scales. With lo = min(0, the
+ * group's least value) and hi = max(0, its greatest): s = (hi - lo) / 15 rounded to
+ * bf16, z = -lo / s and q = w / s + z, both rounded to nearest (ties to even) before
+ * the sum and clamped to 0..15; zeros NULL: s = max |w| / 7 rounded to bf16,
+ * z = 8. Where s rounds to 0 the group is zeros (s = 1); an infinity or NaN in
+ * a group makes its scale NaN.
+ *
+ * colibri_moe_dequantize_int4 gives the values back, bf16 (rounded) or fp32
+ * (exact), from bf16 or fp16 scales: what a layer's init takes.
+ *
+ * Caller-owned DEVICE buffers, w, scales and zeros aligned to their type, codes
+ * 4 bytes, out 16. rows >= 1, rows * cols <= 2^40, rows * row_stride <= 2^42,
+ * row_stride >= cols; otherwise INVALID_ARG. Both enqueue on hip_stream (NULL =
+ * default stream) and return without waiting. They need no handle. */
+colibri_moe_status_t colibri_moe_quantize_int4(const void* w, colibri_moe_dtype_t dtype, int64_t rows, int64_t cols,
+                                               int64_t row_stride, int32_t group, uint8_t* codes, uint16_t* scales,
+                                               uint8_t* zeros, void* hip_stream);
+colibri_moe_status_t colibri_moe_dequantize_int4(const uint8_t* codes, const uint16_t* scales,
+                                                 colibri_moe_dtype_t scale_dtype, const uint8_t* zeros, int64_t rows,
+                                                 int64_t cols, int32_t group, colibri_moe_dtype_t dtype, void* out,
+                                                 void* hip_stream);
+
+/* Products of a few rows with such weights, from the weights as they are: one
+ * matrix [rows][cols], or one per expert. The weights are first laid out for the
+ * kernels, once: colibri_moe_int4_bytes gives the size of the layout (-1: not
+ * supported), colibri_moe_int4_pack fills it (16-byte aligned). */
+typedef struct {
+    int32_t n_experts; /* 1..256 */
+    int32_t rows;      /* N, 1..2^24; even with swiglu */
+    int32_t cols;      /* K, a multiple of 32, at most 2^20; n_experts*rows*cols <= 2^40 */
+    int32_t group;
+    colibri_moe_dtype_t scale_dtype; /* BF16 or F16 */
+    int32_t swiglu;    /* 1: rows 0..N/2-1 are a gate projection, the others up; 0 */
+} colibri_moe_int4_t;
+int64_t colibri_moe_int4_bytes(const colibri_moe_int4_t* m);
+colibri_moe_status_t colibri_moe_int4_pack(const colibri_moe_int4_t* m, const uint8_t* codes, const uint16_t* scales,
+                                           const uint8_t* zeros, void* packed, void* hip_stream);
+
+/* y = W x on packed weights, for T tokens of k slots:
+ *   ids NULL (n_experts and k 1): y[t] = W x[t];
+ *   ids [T][k]: y[t][j] = W[ids[t][j]] x[t], or of x[t][j] with x_per_slot (x [T][k][K]);
+ *   with swiglu, of each row's N values g (first half) and u: SiLU(g) * u, N/2 values;
+ *   with weights [T][k] (not with swiglu): y[t] = sum_j weights[t][j] W[ids[t][j]] x.
+ * x bf16, y bf16 or fp32 (y_dtype), dense. An id outside 0..n_experts-1 marks a
+ * slot without an expert: its row of y is 0, and it adds nothing to a weighted
+ * sum. Ids may repeat. Weights enter the products unrounded; sums are fp32 and
+ * depend on a row's own x, matrix and (weighted) slots alone. x must be below
+ * 2^120 in magnitude; a row with an infinity or NaN gives NaN. T >= 0 (0:
+ * nothing to do), k 1..8, T * k <= COLIBRI_MOE_INT4_ROWS (TOO_LARGE). packed
+ * and x 16-byte, ids, weights and fp32 y 4-byte, bf16 y 2-byte aligned.
+ * Caller-owned DEVICE buffers. Enqueues on hip_stream (NULL = default stream)
+ * and returns without waiting. Needs no handle and no memory of its own. */
+colibri_moe_status_t colibri_moe_int4_linear(const colibri_moe_int4_t* m, const void* packed, const void* x, int32_t T,
+                                             int32_t k, int32_t x_per_slot, const int32_t* ids, const float* weights,
+                                             void* y, colibri_moe_dtype_t y_dtype, void* hip_stream);
 
 /* Measurement helper, not a step of the layer: copies `bytes` bytes from src
  * to dst (caller-owned DEVICE buffers, 16-byte aligned, not overlapping;

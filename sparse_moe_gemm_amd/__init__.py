@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(HERE, "libcolibri_moe.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_OUT_OF_MEMORY, ERR_HIP, ERR_TOO_LARGE = range(7)
 STATIC_SCRATCH_BYTES = 64 << 20  # COLIBRI_MOE_STATIC_SCRATCH_BYTES
 FEW_TOKENS = 16  # COLIBRI_MOE_FEW_TOKENS
-F32, BF16 = 0, 1
+INT4_ROWS = 128  # COLIBRI_MOE_INT4_ROWS
+F32, BF16, F16 = 0, 1, 2
 FLAG_ASYNC = 1 << 0
 FLAG_STAGE_TIMING = 1 << 1
 FLAG_FP8_WEIGHTS = 1 << 2
@@ -58,11 +59,17 @@ class Norm(ctypes.Structure):
                 ("residual_out_stride", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class Int4(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int), ("swiglu", ctypes.c_int32)]
+
+
 EXPORTS = ("colibri_moe_init", "colibri_moe_init_rule", "colibri_moe_forward", "colibri_moe_forward_static",
            "colibri_moe_forward_few", "colibri_moe_free",
            "colibri_moe_status_string", "colibri_moe_stage_times", "colibri_moe_stage_name",
            "colibri_moe_quantize_fp8", "colibri_moe_quantize_mxfp4", "colibri_moe_dequantize_mxfp4",
-           "colibri_moe_route", "colibri_moe_rms_norm", "colibri_moe_stream_copy")
+           "colibri_moe_route", "colibri_moe_rms_norm", "colibri_moe_quantize_int4", "colibri_moe_dequantize_int4",
+           "colibri_moe_int4_bytes", "colibri_moe_int4_pack", "colibri_moe_int4_linear", "colibri_moe_stream_copy")
 
 _lib = None
 
@@ -106,6 +113,17 @@ def lib() -> ctypes.CDLL:
         L.colibri_moe_route.argtypes = [P, ctypes.c_int, ctypes.c_int64, i32, i32, i32, ctypes.POINTER(Rule), P, P, P, P]
         L.colibri_moe_rms_norm.restype = ctypes.c_int
         L.colibri_moe_rms_norm.argtypes = [ctypes.POINTER(Norm), P]
+        i64, I4 = ctypes.c_int64, ctypes.POINTER(Int4)
+        L.colibri_moe_quantize_int4.restype = ctypes.c_int
+        L.colibri_moe_quantize_int4.argtypes = [P, ctypes.c_int, i64, i64, i64, i32, P, P, P, P]
+        L.colibri_moe_dequantize_int4.restype = ctypes.c_int
+        L.colibri_moe_dequantize_int4.argtypes = [P, P, ctypes.c_int, P, i64, i64, i32, ctypes.c_int, P, P]
+        L.colibri_moe_int4_bytes.restype = i64
+        L.colibri_moe_int4_bytes.argtypes = [I4]
+        L.colibri_moe_int4_pack.restype = ctypes.c_int
+        L.colibri_moe_int4_pack.argtypes = [I4, P, P, P, P, P]
+        L.colibri_moe_int4_linear.restype = ctypes.c_int
+        L.colibri_moe_int4_linear.argtypes = [I4, P, P, i32, i32, i32, P, P, P, ctypes.c_int, P]
         L.colibri_moe_stream_copy.restype = ctypes.c_int
         L.colibri_moe_stream_copy.argtypes = [P, P, ctypes.c_int64, P]
         _lib = L
@@ -472,6 +490,217 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
     if st != OK:
         raise ColibriError("colibri_moe_rms_norm", st)
     return out
+
+
+def colibri_moe_quantize_int4(w_ptr: int, dtype: int, rows: int, cols: int, row_stride: int, group: int, codes_ptr: int,
+                              scales_ptr: int, zeros_ptr, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_quantize_int4(w_ptr, dtype, rows, cols, row_stride, group, codes_ptr, scales_ptr, zeros_ptr,
+                                           hip_stream)
+
+
+def colibri_moe_dequantize_int4(codes_ptr: int, scales_ptr: int, scale_dtype: int, zeros_ptr, rows: int, cols: int,
+                                group: int, dtype: int, out_ptr: int, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_dequantize_int4(codes_ptr, scales_ptr, scale_dtype, zeros_ptr, rows, cols, group, dtype,
+                                             out_ptr, hip_stream)
+
+
+def colibri_moe_int4_bytes(m: Int4) -> int:
+    return lib().colibri_moe_int4_bytes(None if m is None else ctypes.byref(m))
+
+
+def colibri_moe_int4_pack(m: Int4, codes_ptr: int, scales_ptr: int, zeros_ptr, packed_ptr: int,
+                          hip_stream: int = 0) -> int:
+    return lib().colibri_moe_int4_pack(None if m is None else ctypes.byref(m), codes_ptr, scales_ptr, zeros_ptr,
+                                       packed_ptr, hip_stream)
+
+
+def colibri_moe_int4_linear(m: Int4, packed_ptr: int, x_ptr: int, T: int, k: int, x_per_slot: int, ids_ptr, weights_ptr,
+                            y_ptr: int, y_dtype: int, hip_stream: int = 0) -> int:
+    return lib().colibri_moe_int4_linear(None if m is None else ctypes.byref(m), packed_ptr, x_ptr, T, k, x_per_slot,
+                                         ids_ptr, weights_ptr, y_ptr, y_dtype, hip_stream)
+
+
+def quantize_int4(w, group=128, symmetric=False, stream=None):
+    """(codes uint8 [..][K/2], scales bf16 [..][K/group], zeros uint8 or None) of
+    a bf16 or fp32 device tensor w, [N][K] with contiguous rows (they may be
+    slices of longer ones) or a contiguous [E][N][K]: 4-bit codes of groups of
+    `group` values (32, 64 or a multiple of 128, dividing K), each with a scale
+    and a zero point (symmetric: none, codes around 8). The work is enqueued on
+    `stream`, by default the current one; a given stream must already be
+    ordered behind the work that makes w."""
+    import torch
+
+    bf16 = w.dtype == torch.bfloat16
+    if not (bf16 or w.dtype == torch.float32) or w.dim() not in (2, 3) or not w.is_cuda:
+        raise TypeError("w must be a 2-D or 3-D bfloat16 or float32 device tensor")
+    *lead, cols = w.shape
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    row_stride = cols
+    if len(lead) == 1:
+        stride, step = w.stride()
+        if (cols > 1 and step != 1) or (rows > 1 and stride < cols):
+            raise ValueError("rows must be contiguous and must not overlap")
+        row_stride = stride if rows > 1 else cols
+    elif not w.is_contiguous():
+        raise ValueError("a 3-D w must be contiguous")
+    if group not in (32, 64) and (group <= 0 or group % 128 != 0) or cols % group != 0:
+        raise ValueError("group must be 32, 64 or a multiple of 128, and divide the row length")
+    if stream is None:
+        def empty(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=w.device)
+    else:
+        empty = _empty_on(stream, w.device)
+        w.record_stream(stream)
+    codes = empty((*lead, cols // 2), torch.uint8)
+    scales = empty((*lead, cols // group), torch.bfloat16)
+    zeros = None if symmetric else empty((*lead, cols // group), torch.uint8)
+    if rows == 0 or cols == 0:
+        return codes, scales, zeros
+    st = _on_device_of(w, colibri_moe_quantize_int4, w.data_ptr(), BF16 if bf16 else F32, rows, cols, row_stride, group,
+                       codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                       _stream_of(w, stream))
+    if st != OK:
+        raise ColibriError("colibri_moe_quantize_int4", st)
+    return codes, scales, zeros
+
+
+def _int4_group(codes, scales, zeros):
+    """Group length of matching contiguous device tensors of 4-bit groups."""
+    import torch
+
+    if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_cuda or not codes.is_contiguous():
+        raise TypeError("codes must be a contiguous 2-D or 3-D uint8 device tensor")
+    if (scales.dtype not in (torch.bfloat16, torch.float16) or scales.device != codes.device
+            or not scales.is_contiguous()):
+        raise TypeError("scales must be a contiguous bfloat16 or float16 tensor on the codes' device")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.device != codes.device or not zeros.is_contiguous()):
+        raise TypeError("zeros must be a contiguous uint8 tensor on the codes' device")
+    cols, groups = codes.shape[-1] * 2, scales.shape[-1] if scales.dim() else 0
+    if (tuple(scales.shape[:-1]) != tuple(codes.shape[:-1]) or groups == 0 or cols % groups != 0
+            or (zeros is not None and tuple(zeros.shape) != tuple(scales.shape))):
+        raise ValueError("codes [..][K/2], scales and zeros [..][K/group] do not belong together")
+    return cols // groups
+
+
+def dequantize_int4(codes, scales, zeros=None, dtype=None, stream=None):
+    """The values [..][K] (bf16 by default, rounded; or fp32, exact) of 4-bit
+    groups as quantize_int4 gives them (scales bf16 or fp16; without zeros every
+    zero point is 8): what MoELayer takes for such weights. The work is
+    enqueued on `stream`, by default the current one; a given stream must
+    already be ordered behind the work that makes the tensors."""
+    import torch
+
+    group = _int4_group(codes, scales, zeros)
+    bf16 = dtype is None or dtype == torch.bfloat16
+    if not (bf16 or dtype == torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    *lead, half = codes.shape
+    rows, cols = lead[0] if len(lead) == 1 else lead[0] * lead[1], half * 2
+    value = torch.bfloat16 if bf16 else torch.float32
+    if stream is None:
+        out = torch.empty((*lead, cols), dtype=value, device=codes.device)
+    else:
+        out = _empty_on(stream, codes.device)((*lead, cols), value)
+        for t in (codes, scales, zeros):
+            if t is not None:
+                t.record_stream(stream)
+    if rows == 0:
+        return out
+    st = _on_device_of(codes, colibri_moe_dequantize_int4, codes.data_ptr(), scales.data_ptr(),
+                       BF16 if scales.dtype == torch.bfloat16 else F16, None if zeros is None else zeros.data_ptr(),
+                       rows, cols, group, BF16 if bf16 else F32, out.data_ptr(), _stream_of(codes, stream))
+    if st != OK:
+        raise ColibriError("colibri_moe_dequantize_int4", st)
+    return out
+
+
+class Int4Linear:
+    """A matrix of 4-bit groups, or one per expert, laid out once for products
+    of few rows (colibri_moe_int4_linear). codes uint8 [N][K/2] or [E][N][K/2],
+    scales bf16 or fp16 and zeros uint8 (or None: 8) [..][K/group], as
+    quantize_int4 gives them; they are copied. swiglu: the first half of the N
+    rows is a gate projection, the second the up projection of the same units.
+    The layout is made on `stream`, by default the current one; calls on other
+    streams must be ordered behind it."""
+
+    def __init__(self, codes, scales, zeros=None, swiglu: bool = False, stream=None):
+        import torch
+
+        group = _int4_group(codes, scales, zeros)
+        *lead, half = codes.shape
+        self.E, self.N, self.K, self.group = (1 if len(lead) == 1 else lead[0]), lead[-1], half * 2, group
+        self.swiglu, self.device = bool(swiglu), codes.device
+        self.out_features = self.N // 2 if swiglu else self.N
+        self.c = Int4(self.E, self.N, self.K, group, BF16 if scales.dtype == torch.bfloat16 else F16, int(self.swiglu))
+        n = colibri_moe_int4_bytes(self.c)
+        if n < 0:
+            raise ValueError("not supported: K must be a multiple of 32, group 32, 64 or a multiple of 128, E at most 256, "
+                             "N even with swiglu")
+        if stream is None:
+            self.packed = torch.empty((n,), dtype=torch.uint8, device=codes.device)
+        else:
+            self.packed = _empty_on(stream, codes.device)((n,), torch.uint8)
+            for t in (codes, scales, zeros):
+                if t is not None:
+                    t.record_stream(stream)
+        st = _on_device_of(codes, colibri_moe_int4_pack, self.c, codes.data_ptr(), scales.data_ptr(),
+                           None if zeros is None else zeros.data_ptr(), self.packed.data_ptr(), _stream_of(codes, stream))
+        if st != OK:
+            raise ColibriError("colibri_moe_int4_pack", st)
+
+    def forward(self, x, ids=None, weights=None, y=None, dtype=None, stream=None):
+        """W x for x bf16 [T][K]. With ids (int32 [T][k], one matrix per expert):
+        y [T][k][n] for x [T][K] or [T][k][K], or with weights (fp32 [T][k], not
+        with swiglu) their weighted sum [T][n]; n is N, or N/2 with swiglu. A slot
+        whose id is outside 0..E-1 gives zeros and adds nothing. At most
+        INT4_ROWS (128) rows T * k. y bf16, or dtype=torch.float32; a given y is
+        written and returned. The work is enqueued on `stream`, by default the
+        current one; a given stream must already be ordered behind the work
+        that makes the tensors."""
+        import torch
+
+        if (x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != self.device or x.dim() not in (2, 3)
+                or x.shape[-1] != self.K):
+            raise TypeError("x must be a contiguous bfloat16 tensor [T][K] or [T][k][K] on the weights' device")
+        T, per_slot, k = x.shape[0], x.dim() == 3, 1
+        if ids is not None:
+            if ids.dtype != torch.int32 or ids.dim() != 2 or not ids.is_contiguous() or ids.device != self.device:
+                raise TypeError("ids must be a contiguous 2-D int32 tensor on the weights' device")
+            k = ids.shape[1]
+            if ids.shape[0] != T or (per_slot and x.shape[1] != k):
+                raise ValueError("ids [T][k] do not fit x")
+        elif self.E != 1 or per_slot or weights is not None:
+            raise ValueError("one matrix per expert, x [T][k][K] and weights need ids")
+        if weights is not None:
+            if (weights.dtype != torch.float32 or tuple(weights.shape) != (T, k) or not weights.is_contiguous()
+                    or weights.device != self.device):
+                raise TypeError("weights must be a contiguous float32 tensor [T][k] on the weights' device")
+            if self.swiglu:
+                raise ValueError("no weighted sum behind swiglu")
+        f32 = dtype == torch.float32
+        if not (f32 or dtype is None or dtype == torch.bfloat16):
+            raise TypeError("dtype must be bfloat16 or float32")
+        shape = (T, self.out_features) if ids is None or weights is not None else (T, k, self.out_features)
+        value = torch.float32 if f32 else torch.bfloat16
+        if y is not None and (y.dtype != value or tuple(y.shape) != shape or not y.is_contiguous()
+                              or y.device != self.device):
+            raise TypeError("y must be a contiguous tensor of the result's shape and dtype on the weights' device")
+        if T * k > INT4_ROWS:
+            raise ColibriError("colibri_moe_int4_linear", ERR_TOO_LARGE)
+        if stream is not None:
+            _check_stream(stream, self.device)
+            for t in (x, ids, weights, y, self.packed):
+                if t is not None:
+                    t.record_stream(stream)
+        if y is None:
+            y = (torch.empty(shape, dtype=value, device=self.device) if stream is None
+                 else _empty_on(stream, self.device)(shape, value))
+        st = _on_device_of(x, colibri_moe_int4_linear, self.c, self.packed.data_ptr(), x.data_ptr(), T, k, int(per_slot),
+                           None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(),
+                           y.data_ptr(), F32 if f32 else BF16, _stream_of(x, stream))
+        if st != OK:
+            raise ColibriError("colibri_moe_int4_linear", st)
+        return y
 
 
 def colibri_moe_stream_copy(src_ptr: int, dst_ptr: int, nbytes: int, hip_stream: int = 0) -> int:

@@ -27,6 +27,7 @@ constexpr uint32_t kMagic = 0xC011B41Eu;
 constexpr int kStages = 6;
 constexpr int32_t kMaxTokensLimit = 1 << 24;
 static_assert(COLIBRI_MOE_FEW_TOKENS == kFewTokens, "header and kernels agree");
+static_assert(COLIBRI_MOE_INT4_ROWS == kInt4Rows, "header and kernels agree");
 
 const char* const kStageNames[kStages] = {"router",         "dispatch",  "gate_up_gemm",
                                           "gate_up_reduce", "down_gemm", "combine"};
@@ -245,6 +246,32 @@ SelectRule select_rule(const colibri_moe_rule_t* r, const float* bias)
 {
     return SelectRule{1, r->scoring == COLIBRI_MOE_SCORE_SIGMOID, r->n_groups, r->top_groups,
                       r->group_score == COLIBRI_MOE_GROUP_TOP2, r->normalize, r->scale, bias};
+}
+
+bool int4_groups_fit(int64_t rows, int64_t cols, int32_t group)
+{
+    return (group == 32 || group == 64 || (group > 0 && group % 128 == 0)) && cols >= group && cols % group == 0 &&
+           cols <= INT32_MAX && rows >= 1 && rows <= ((int64_t)1 << 40) / cols;
+}
+
+bool int4_fits(const colibri_moe_int4_t& m)
+{
+    return m.n_experts >= 1 && m.n_experts <= kMaxExperts && m.rows >= 1 && m.rows <= 1 << 24 && m.cols <= 1 << 20 &&
+           int4_groups_fit((int64_t)m.n_experts * m.rows, m.cols, m.group) &&
+           (m.scale_dtype == COLIBRI_MOE_BF16 || m.scale_dtype == COLIBRI_MOE_F16) &&
+           (m.swiglu == 0 || (m.swiglu == 1 && m.rows % 2 == 0));
+}
+
+// Compute units of the current device; 0 if it cannot be asked.
+int current_cus()
+{
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return 0;
+    }
+    return cus;
 }
 
 #define CMOE_HIP(call)                      \
@@ -927,6 +954,87 @@ colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip
     return COLIBRI_MOE_OK;
 }
 
+colibri_moe_status_t colibri_moe_quantize_int4(const void* w, colibri_moe_dtype_t dtype, int64_t rows, int64_t cols,
+                                               int64_t row_stride, int32_t group, uint8_t* codes, uint16_t* scales,
+                                               uint8_t* zeros, void* hip_stream)
+{
+    if (!w || !codes || !scales || !int4_groups_fit(rows, cols, group) || row_stride < cols ||
+        row_stride > ((int64_t)1 << 42) / rows || (dtype != COLIBRI_MOE_BF16 && dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)w & (dtype == COLIBRI_MOE_BF16 ? 1u : 3u)) || ((uintptr_t)codes & 3u) || ((uintptr_t)scales & 1u))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    CMOE_HIP(launch_int4_quantize(w, dtype == COLIBRI_MOE_BF16, rows, cols, row_stride, group, codes, scales, zeros,
+                                  (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_dequantize_int4(const uint8_t* codes, const uint16_t* scales,
+                                                 colibri_moe_dtype_t scale_dtype, const uint8_t* zeros, int64_t rows,
+                                                 int64_t cols, int32_t group, colibri_moe_dtype_t dtype, void* out,
+                                                 void* hip_stream)
+{
+    if (!codes || !scales || !out || !int4_groups_fit(rows, cols, group) ||
+        (scale_dtype != COLIBRI_MOE_BF16 && scale_dtype != COLIBRI_MOE_F16) ||
+        (dtype != COLIBRI_MOE_BF16 && dtype != COLIBRI_MOE_F32))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)codes & 3u) || ((uintptr_t)scales & 1u) || !aligned16(out))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    CMOE_HIP(launch_int4_dequantize(codes, scales, scale_dtype == COLIBRI_MOE_F16, zeros, rows, cols, group,
+                                    dtype == COLIBRI_MOE_BF16, out, (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+int64_t colibri_moe_int4_bytes(const colibri_moe_int4_t* m)
+{
+    if (!m || !int4_fits(*m))
+        return -1;
+    return (int64_t)(round_up(int4_code_bytes(m->n_experts, m->rows, m->cols, m->swiglu), 256) +
+                     int4_meta_bytes(m->n_experts, m->rows, m->cols, m->group, m->swiglu));
+}
+
+colibri_moe_status_t colibri_moe_int4_pack(const colibri_moe_int4_t* m, const uint8_t* codes, const uint16_t* scales,
+                                           const uint8_t* zeros, void* packed, void* hip_stream)
+{
+    if (!m || !int4_fits(*m) || !codes || !scales || !packed)
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)scales & 1u) || !aligned16(packed))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    const size_t at = round_up(int4_code_bytes(m->n_experts, m->rows, m->cols, m->swiglu), 256);
+    const Int4Pack p{codes, scales, zeros, m->n_experts, m->rows, m->cols, m->group, m->swiglu,
+                     (uint32_t*)packed, (uint32_t*)((uint8_t*)packed + at)};
+    CMOE_HIP(launch_int4_pack(p, (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
+colibri_moe_status_t colibri_moe_int4_linear(const colibri_moe_int4_t* m, const void* packed, const void* x, int32_t T,
+                                             int32_t k, int32_t x_per_slot, const int32_t* ids, const float* weights,
+                                             void* y, colibri_moe_dtype_t y_dtype, void* hip_stream)
+{
+    if (!m || !int4_fits(*m) || T < 0 || k < 1 || (x_per_slot != 0 && x_per_slot != 1) ||
+        (y_dtype != COLIBRI_MOE_BF16 && y_dtype != COLIBRI_MOE_F32) || (weights && m->swiglu))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (k > kMaxTopK)
+        return COLIBRI_MOE_ERR_UNSUPPORTED;
+    if ((int64_t)T * k > COLIBRI_MOE_INT4_ROWS)
+        return COLIBRI_MOE_ERR_TOO_LARGE;
+    if (T == 0)
+        return COLIBRI_MOE_OK;
+    if (!packed || !x || !y || (!ids && (m->n_experts != 1 || k != 1 || weights)))
+        return COLIBRI_MOE_ERR_INVALID_ARG;
+    if (!aligned16(packed) || !aligned16(x) || ((uintptr_t)ids & 3u) || ((uintptr_t)weights & 3u) ||
+        ((uintptr_t)y & (y_dtype == COLIBRI_MOE_BF16 ? 1u : 3u)))
+        return COLIBRI_MOE_ERR_ALIGNMENT;
+    const int cus = current_cus();
+    if (cus <= 0)
+        return COLIBRI_MOE_ERR_HIP;
+    const size_t at = round_up(int4_code_bytes(m->n_experts, m->rows, m->cols, m->swiglu), 256);
+    const Int4Args a{packed, (const uint8_t*)packed + at, m->n_experts, m->rows, m->cols, m->group,
+                     m->scale_dtype == COLIBRI_MOE_F16, m->swiglu, x, x_per_slot, T, k, ids, weights, y,
+                     y_dtype == COLIBRI_MOE_F32};
+    CMOE_HIP(launch_int4_linear(a, cus, (hipStream_t)hip_stream));
+    return COLIBRI_MOE_OK;
+}
+
 colibri_moe_status_t colibri_moe_stream_copy(const void* src, void* dst, int64_t bytes, void* hip_stream)
 {
     if (!src || !dst || bytes < 16 || bytes % 16 != 0)
@@ -936,12 +1044,9 @@ colibri_moe_status_t colibri_moe_stream_copy(const void* src, void* dst, int64_t
     const uint8_t *s0 = (const uint8_t*)src, *d0 = (const uint8_t*)dst;
     if (s0 < d0 + bytes && d0 < s0 + bytes)
         return COLIBRI_MOE_ERR_INVALID_ARG;
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) !=
-                                                hipSuccess || cus <= 0) {
-        (void)hipGetLastError();
+    const int cus = current_cus();
+    if (cus <= 0)
         return COLIBRI_MOE_ERR_HIP;
-    }
     CMOE_HIP(launch_stream_copy(src, dst, bytes, cus, (hipStream_t)hip_stream));
     return COLIBRI_MOE_OK;
 }

@@ -319,6 +319,42 @@ int64_t mx_split_rows(int cus);  // calls of more assignments are not split
 hipError_t launch_gate_up_mx(const MxGemmArgs& a, hipStream_t s);
 hipError_t launch_down_mx(const MxGemmArgs& a, hipStream_t s);
 
+// 4-bit integer groups (quant_int4.hip): codes [rows][cols/2], bf16 scales and
+// zero points (null: symmetric) [rows][cols/group] of bf16 or fp32 rows (row r
+// at w + r * ld elements), and back. group: 32, 64 or a multiple of 128.
+hipError_t launch_int4_quantize(const void* w, int bf16_in, int64_t rows, int64_t cols, int64_t ld, int group,
+                                uint8_t* codes, uint16_t* scales, uint8_t* zeros, hipStream_t s);
+hipError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, int scales_f16, const uint8_t* zeros,
+                                  int64_t rows, int64_t cols, int group, int bf16_out, void* out, hipStream_t s);
+
+// Products with such weights [E][N][K] (int4.hip) in their own layout: its two
+// parts' sizes, and the repack of the caller's.
+size_t int4_code_bytes(int E, int N, int K, int swiglu);
+size_t int4_meta_bytes(int E, int N, int K, int group, int swiglu);
+struct Int4Pack {
+    const uint8_t* codes;
+    const uint16_t* scales;
+    const uint8_t* zeros;  // or null: 8
+    int E, N, K, group, swiglu;
+    uint32_t* out_codes;
+    uint32_t* out_meta;
+};
+hipError_t launch_int4_pack(const Int4Pack& p, hipStream_t s);
+constexpr int kInt4Rows = 128;  // most assignments T * k of a call
+struct Int4Args {
+    const void* codes;     // packed
+    const void* meta;
+    int E, N, K, group, scales_f16, swiglu;
+    const void* x;         // bf16 [T][K], or x_per_slot: [T][k][K]
+    int x_per_slot;
+    int T, k;
+    const int32_t* ids;    // [T][k], or null: one matrix, k = 1
+    const float* w;        // [T][k]: weighted sum over a token's slots, or null
+    void* y;
+    int y_f32;             // y fp32, else bf16
+};
+hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s);
+
 // The whole layer for at most kFewTokens tokens in two launches (few.hip),
 // bf16 layers of any weight precision.
 constexpr int kFewTokens = 16;

@@ -229,3 +229,208 @@ def test_plain_routing_on_hand_worked_tokens():
     assert ids.tolist() == [[0, 1]] and w.tolist() == [[1, 0]]
     ids, w, _, _ = route_ref.route([[-np.inf] * 4], 3)
     assert ids.tolist() == [[0, 1, 2]] and w.tolist() == [[0, 0, 0]]
+
+
+# --- 4-bit integer groups -------------------------------------------------------------------------
+
+
+def c_quant(w=FAKE, dtype=cm.BF16, rows=4, cols=256, stride=256, group=128, codes=FAKE, scales=FAKE, zeros=FAKE):
+    return cm.colibri_moe_quantize_int4(w, dtype, rows, cols, stride, group, codes, scales, zeros)
+
+
+def c_dequant(codes=FAKE, scales=FAKE, sd=cm.BF16, zeros=FAKE, rows=4, cols=256, group=128, dtype=cm.BF16, out=FAKE):
+    return cm.colibri_moe_dequantize_int4(codes, scales, sd, zeros, rows, cols, group, dtype, out)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(w=None), cm.ERR_INVALID_ARG), (dict(codes=None), cm.ERR_INVALID_ARG), (dict(scales=None), cm.ERR_INVALID_ARG),
+    (dict(dtype=cm.F16), cm.ERR_INVALID_ARG), (dict(rows=0), cm.ERR_INVALID_ARG), (dict(cols=0), cm.ERR_INVALID_ARG),
+    (dict(cols=192, stride=192), cm.ERR_INVALID_ARG), (dict(stride=255), cm.ERR_INVALID_ARG),
+    (dict(group=0), cm.ERR_INVALID_ARG), (dict(group=16), cm.ERR_INVALID_ARG), (dict(group=96), cm.ERR_INVALID_ARG),
+    (dict(group=512), cm.ERR_INVALID_ARG), (dict(group=-128), cm.ERR_INVALID_ARG),
+    (dict(rows=(1 << 40) // 256 + 1), cm.ERR_INVALID_ARG), (dict(stride=1 << 41), cm.ERR_INVALID_ARG),
+    (dict(w=FAKE + 1), cm.ERR_ALIGNMENT), (dict(w=FAKE + 2, dtype=cm.F32), cm.ERR_ALIGNMENT),
+    (dict(codes=FAKE + 2), cm.ERR_ALIGNMENT), (dict(scales=FAKE + 1), cm.ERR_ALIGNMENT),
+])
+def test_quantize_int4_refusals(kw, status):
+    assert c_quant(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(codes=None), cm.ERR_INVALID_ARG), (dict(scales=None), cm.ERR_INVALID_ARG), (dict(out=None), cm.ERR_INVALID_ARG),
+    (dict(sd=cm.F32), cm.ERR_INVALID_ARG), (dict(dtype=cm.F16), cm.ERR_INVALID_ARG), (dict(rows=0), cm.ERR_INVALID_ARG),
+    (dict(group=48), cm.ERR_INVALID_ARG), (dict(cols=384, group=256), cm.ERR_INVALID_ARG),
+    (dict(codes=FAKE + 2), cm.ERR_ALIGNMENT), (dict(scales=FAKE + 1), cm.ERR_ALIGNMENT), (dict(out=FAKE + 8), cm.ERR_ALIGNMENT),
+])
+def test_dequantize_int4_refusals(kw, status):
+    assert c_dequant(**kw) == status
+
+
+def matrix(**kw):
+    a = dict(n_experts=4, rows=64, cols=256, group=128, scale_dtype=cm.BF16, swiglu=0)
+    a.update(kw)
+    return cm.Int4(*a.values())
+
+
+BAD_MATRICES = [dict(n_experts=0), dict(n_experts=257), dict(rows=0), dict(rows=(1 << 24) + 1), dict(cols=0),
+                dict(cols=320), dict(cols=1 << 21), dict(group=16), dict(group=192), dict(scale_dtype=cm.F32),
+                dict(swiglu=2), dict(swiglu=1, rows=63), dict(n_experts=256, rows=1 << 24, cols=512)]
+
+
+def c_linear(m=None, packed=FAKE, x=FAKE, T=4, k=2, per_slot=0, ids=FAKE, weights=None, y=FAKE, dtype=cm.BF16):
+    return cm.colibri_moe_int4_linear(m or matrix(), packed, x, T, k, per_slot, ids, weights, y, dtype)
+
+
+@pytest.mark.parametrize("bad", BAD_MATRICES, ids=str)
+def test_matrices_that_are_not_supported(bad):
+    m = matrix(**bad)
+    assert cm.colibri_moe_int4_bytes(m) == -1
+    assert cm.colibri_moe_int4_pack(m, FAKE, FAKE, None, FAKE) == cm.ERR_INVALID_ARG
+    assert c_linear(m) == cm.ERR_INVALID_ARG
+
+
+def test_pack_refusals_and_sizes():
+    m = matrix()
+    for args in ((None, FAKE, None, FAKE), (FAKE, None, None, FAKE), (FAKE, FAKE, None, None)):
+        assert cm.colibri_moe_int4_pack(m, *args) == cm.ERR_INVALID_ARG
+    assert cm.colibri_moe_int4_pack(None, FAKE, FAKE, None, FAKE) == cm.ERR_INVALID_ARG
+    assert cm.colibri_moe_int4_bytes(None) == -1
+    assert cm.colibri_moe_int4_pack(m, FAKE, FAKE + 1, None, FAKE) == cm.ERR_ALIGNMENT
+    assert cm.colibri_moe_int4_pack(m, FAKE, FAKE, None, FAKE + 8) == cm.ERR_ALIGNMENT
+    # whole tiles: half a byte per code, four bytes per group
+    assert cm.colibri_moe_int4_bytes(m) == 4 * 64 * (256 // 2 + 4 * 2)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(packed=None), cm.ERR_INVALID_ARG), (dict(x=None), cm.ERR_INVALID_ARG), (dict(y=None), cm.ERR_INVALID_ARG),
+    (dict(T=-1), cm.ERR_INVALID_ARG), (dict(k=0), cm.ERR_INVALID_ARG), (dict(per_slot=2), cm.ERR_INVALID_ARG),
+    (dict(dtype=cm.F16), cm.ERR_INVALID_ARG), (dict(ids=None), cm.ERR_INVALID_ARG),
+    (dict(m=matrix(n_experts=1), ids=None), cm.ERR_INVALID_ARG),
+    (dict(m=matrix(n_experts=1), ids=None, k=1, weights=FAKE), cm.ERR_INVALID_ARG),
+    (dict(m=matrix(swiglu=1), weights=FAKE), cm.ERR_INVALID_ARG), (dict(k=9), cm.ERR_UNSUPPORTED),
+    (dict(T=65), cm.ERR_TOO_LARGE), (dict(T=1 << 30, k=8), cm.ERR_TOO_LARGE), (dict(packed=FAKE + 8), cm.ERR_ALIGNMENT),
+    (dict(x=FAKE + 8), cm.ERR_ALIGNMENT), (dict(ids=FAKE + 2), cm.ERR_ALIGNMENT), (dict(weights=FAKE + 2), cm.ERR_ALIGNMENT),
+    (dict(y=FAKE + 1), cm.ERR_ALIGNMENT), (dict(y=FAKE + 2, dtype=cm.F32), cm.ERR_ALIGNMENT),
+    (dict(T=0, packed=None, x=None, y=None), cm.OK),
+])
+def test_int4_linear_refusals(kw, status):
+    assert c_linear(**kw) == status
+    assert cm.colibri_moe_int4_linear(None, FAKE, FAKE, 4, 2, 0, FAKE, None, FAKE, cm.BF16) == cm.ERR_INVALID_ARG
+
+
+def test_int4_codec_arguments(dev, monkeypatch):
+    calls = []
+    for fn in ("colibri_moe_quantize_int4", "colibri_moe_dequantize_int4"):
+        monkeypatch.setattr(cm, fn, lambda *a: calls.append(a) or cm.OK)
+    for bad in (torch.zeros(4, 256, dtype=BF16), tensor(dev, (4, 256), torch.float16), tensor(dev, (256,), BF16)):
+        with pytest.raises(TypeError):
+            cm.quantize_int4(bad)
+    for bad, group in ((tensor(dev, (4, 256), BF16, stride=(255, 1)), 128), (tensor(dev, (4, 256), BF16, stride=(512, 2)), 128),
+                       (tensor(dev, (2, 4, 256), BF16, stride=(2048, 256, 1)), 128), (tensor(dev, (4, 256), BF16), 96),
+                       (tensor(dev, (4, 192), BF16), 128), (tensor(dev, (4, 256), BF16), 0)):
+        with pytest.raises(ValueError):
+            cm.quantize_int4(bad, group)
+    s = fake_device.Stream(0x74)
+    with pytest.raises(ValueError):
+        cm.quantize_int4(tensor(dev, (4, 256), BF16), stream=fake_device.Stream(0x75, index=1))
+    assert not calls
+    w = tensor(dev, (2, 4, 256), F32)
+    codes, scales, zeros = cm.quantize_int4(w, 64, stream=s)
+    assert calls[-1] == (w.ptr, cm.F32, 8, 256, 256, 64, codes.ptr, scales.ptr, zeros.ptr, 0x74)
+    assert (codes.shape, scales.shape, zeros.shape) == ((2, 4, 128), (2, 4, 4), (2, 4, 4))
+    assert all(t.pool is s and dev.current in t.recorded for t in (codes, scales, zeros)) and s in w.recorded
+    assert cm.quantize_int4(w, symmetric=True)[2] is None and calls[-1][8] is None
+    good = dict(codes=tensor(dev, (4, 128), U8), scales=tensor(dev, (4, 2), BF16), zeros=tensor(dev, (4, 2), U8))
+    n = len(calls)
+    for name, bad in (("codes", tensor(dev, (4, 128), I32)), ("codes", tensor(dev, (128,), U8)),
+                      ("codes", tensor(dev, (4, 128), U8, stride=(256, 1))), ("scales", tensor(dev, (4, 2), F32)),
+                      ("scales", tensor(dev, (4, 2), BF16, index=1)), ("zeros", tensor(dev, (4, 2), I32)),
+                      ("zeros", tensor(dev, (4, 2), U8, index=1))):
+        for fn in (cm.dequantize_int4, cm.Int4Linear):
+            with pytest.raises(TypeError):
+                fn(**{**good, name: bad})
+    for name, bad in (("codes", tensor(dev, (5, 128), U8)), ("scales", tensor(dev, (4, 3), BF16)),
+                      ("scales", tensor(dev, (4, 0), BF16)), ("zeros", tensor(dev, (4, 1), U8))):
+        for fn in (cm.dequantize_int4, cm.Int4Linear):
+            with pytest.raises(ValueError):
+                fn(**{**good, name: bad})
+    with pytest.raises(TypeError):
+        cm.dequantize_int4(**good, dtype=torch.float16)
+    assert len(calls) == n
+    out = cm.dequantize_int4(**good, stream=s)
+    assert calls[-1][-2:] == (out.ptr, 0x74) and out.pool is s and all(s in t.recorded for t in good.values())
+
+
+def test_int4_linear_arguments(dev, monkeypatch):
+    calls = []
+    monkeypatch.setattr(cm, "colibri_moe_int4_pack", lambda *a: cm.OK)
+    monkeypatch.setattr(cm, "colibri_moe_int4_linear", lambda *a: calls.append(a) or cm.OK)
+
+    def linear(E=4, N=64, K=256, **kw):
+        lead = (N,) if E is None else (E, N)
+        return cm.Int4Linear(tensor(dev, (*lead, K // 2), U8), tensor(dev, (*lead, K // 128), BF16), **kw)
+
+    with pytest.raises(ValueError):
+        linear(N=63, swiglu=True)
+    lin, dense = linear(), linear(None)
+    x, ids, w = tensor(dev, (5, 256), BF16), tensor(dev, (5, 2), I32), tensor(dev, (5, 2), F32)
+    for bad in (tensor(dev, (5, 256), F32), tensor(dev, (5, 255), BF16), tensor(dev, (256,), BF16),
+                tensor(dev, (5, 256), BF16, index=1), tensor(dev, (5, 256), BF16, stride=(512, 1))):
+        with pytest.raises(TypeError):
+            lin.forward(bad, ids)
+    for bad in (tensor(dev, (5, 2), torch.int64), tensor(dev, (10,), I32), tensor(dev, (5, 2), I32, index=1),
+                tensor(dev, (5, 2), I32, stride=(4, 1))):
+        with pytest.raises(TypeError):
+            lin.forward(x, bad)
+    for bad in (tensor(dev, (5, 2), BF16), tensor(dev, (5, 3), F32), tensor(dev, (5, 2), F32, index=1)):
+        with pytest.raises(TypeError):
+            lin.forward(x, ids, bad)
+    with pytest.raises(ValueError):
+        lin.forward(x)
+    with pytest.raises(ValueError):
+        lin.forward(x, tensor(dev, (4, 2), I32))
+    with pytest.raises(ValueError):
+        lin.forward(tensor(dev, (5, 3, 256), BF16), ids)
+    with pytest.raises(ValueError):
+        dense.forward(tensor(dev, (5, 1, 256), BF16))
+    with pytest.raises(ValueError):
+        dense.forward(x, weights=w)
+    with pytest.raises(ValueError):
+        linear(swiglu=True).forward(x, ids, w)
+    with pytest.raises(TypeError):
+        lin.forward(x, ids, dtype=torch.float16)
+    for bad in (tensor(dev, (5, 2, 64), F32), tensor(dev, (5, 64), BF16), tensor(dev, (5, 2, 64), BF16, index=1),
+                tensor(dev, (5, 2, 64), BF16, stride=(256, 64, 1))):
+        with pytest.raises(TypeError):
+            lin.forward(x, ids, y=bad)
+    with pytest.raises(cm.ColibriError):
+        lin.forward(tensor(dev, (65, 256), BF16), tensor(dev, (65, 2), I32))
+    with pytest.raises(ValueError):
+        lin.forward(x, ids, stream=fake_device.Stream(0x76, index=1))
+    assert not calls
+    y = lin.forward(x, ids)
+    assert y.shape == (5, 2, 64) and calls[-1][2:6] == (x.ptr, 5, 2, 0)
+    assert lin.forward(x, ids, w, dtype=F32).shape == (5, 64)
+    assert linear(swiglu=True).forward(tensor(dev, (5, 2, 256), BF16), ids).shape == (5, 2, 32) and calls[-1][5] == 1
+    assert dense.forward(x).shape == (5, 64)
+    s = fake_device.Stream(0x77)
+    y = lin.forward(x, ids, w, stream=s)
+    assert calls[-1][-1] == 0x77 and y.pool is s and dev.current in y.recorded
+    assert all(s in t.recorded for t in (x, ids, w, lin.packed))
+
+
+def test_plain_int4_on_hand_worked_groups():
+    import int4_ref
+
+    w = np.zeros((2, 32))
+    w[0, :3] = [-1.0, 2.0, 0.5]       # lo -1, hi 2: s = 0.2 as bf16, z = 5
+    w[1, :2] = [7.0, -3.5]
+    q, s, z, _ = int4_ref.quantize(w, 32, False)
+    assert s[0, 0] == int4_ref.to_bf16(0.2) == 0.2001953125 and z[0, 0] == 5
+    assert q[0, :4].tolist() == [0, 15, 7, 5]  # 2 / s = 9.99: 10 steps; 0.5 / s = 2.5 - : 2
+    q, s, z, _ = int4_ref.quantize(w, 32, True)
+    assert s[1, 0] == 1 and q[1, :3].tolist() == [15, 4, 8]  # -3.5: a tie, to -4
+    assert int4_ref.values(q, s, None)[1, :3].tolist() == [7, -4, 0]
+    assert (int4_ref.unpack(int4_ref.pack(q)) == q).all()
+    y, _ = int4_ref.product64(np.eye(32)[:2], q, s, None)
+    assert y[:, 1].tolist() == [7, -4]
