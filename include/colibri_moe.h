@@ -393,9 +393,10 @@ colibri_moe_status_t colibri_moe_int4_pack(const colibri_moe_int4_t* m, const ui
  *   with weights [T][k] (not with swiglu): y[t] = sum_j weights[t][j] W[ids[t][j]] x.
  * x bf16, y bf16 or fp32 (y_dtype), dense. An id outside 0..n_experts-1 marks a
  * slot without an expert: its row of y is 0, and it adds nothing to a weighted
- * sum. Ids may repeat. Weights enter the products unrounded; sums are fp32 and
- * depend on a row's own x, matrix and (weighted) slots alone. x must be below
- * 2^120 in magnitude; a row with an infinity or NaN gives NaN. T >= 0 (0:
+ * sum. Ids may repeat. Weights enter the products unrounded; sums are fp32, in
+ * an order that the call's sizes and ids decide (the same call gives the same
+ * bits), and no row's values reach another row. x must be below
+ * 2^115 in magnitude; a row with an infinity or NaN gives NaN. T >= 0 (0:
  * nothing to do), k 1..8, T * k <= COLIBRI_MOE_INT4_ROWS (TOO_LARGE). packed
  * and x 16-byte, ids, weights and fp32 y 4-byte, bf16 y 2-byte aligned.
  * Caller-owned DEVICE buffers. Enqueues on hip_stream (NULL = default stream)

@@ -31,8 +31,6 @@ namespace {
 constexpr int kUnitK = 128;
 constexpr int kMaxRows = kInt4Rows;
 
-enum Form { kPlain = 0, kSwiglu = 1, kWeighted = 2 };
-
 __host__ __device__ __forceinline__ int units_of(int K) { return (K + kUnitK - 1) / kUnitK; }
 
 // Tiles of 16 rows, an even number (a work item takes one or two). SwiGLU: gate
@@ -46,9 +44,9 @@ __host__ __device__ __forceinline__ int tiles_of(int N, int swiglu)
 __host__ __device__ __forceinline__ int unit_groups(int group) { return group == 32 ? 4 : group == 64 ? 2 : 1; }
 
 // Eight codes of a word as bf16 16 + q: element 2p is nibble p, 2p + 1 nibble p + 4.
-__device__ __forceinline__ bf16x8 codes8(uint32_t w)
+// (m: the place of four mantissa bits in both halves, b: 16.0 in both).
+__device__ __forceinline__ bf16x8 codes8(uint32_t w, uint32_t m, uint32_t b)
 {
-    const uint32_t m = 0x00780078u, b = 0x41804180u;
     const Vec16 v = {((w << 3) & m) | b, ((w >> 1) & m) | b, ((w >> 5) & m) | b, ((w >> 9) & m) | b};
     return as_bf16x8(v);
 }
@@ -104,53 +102,97 @@ __global__ __launch_bounds__(256) void int4_pack_kernel(Int4Pack p, int units, i
     }
 }
 
-// Assignments by expert: order[] lists them expert by expert; pass i is up to
-// CP of them, from order[start[i]], with the same expert.
-struct Passes {
-    int32_t id[kMaxRows];
+// Assignments by expert: row r is the r-th of them, expert by expert; a pass is
+// up to CP of them with the same expert.
+struct Pass {
+    int16_t expert, start, count, unused;
+};
+struct Row {
+    uint32_t x;       // byte offset of its row of x
+    int16_t assigned;  // t * k + j
+    int16_t token;
+    float w;
+    uint32_t unused;
+};
+struct __align__(16) Passes {
+    Row row[kMaxRows];
+    Pass pass[kMaxRows];
+    int32_t key[kMaxRows];
+    uint32_t counts[kMaxRows];
     uint32_t mask[kMaxRows / 32];
-    int16_t order[kMaxRows], start[kMaxRows], count[kMaxRows], expert[kMaxRows];
+    int32_t none;    // some assignment is of no expert
+    int32_t twins;   // some token has an expert in two slots
 };
 
-// Number of passes. An id outside 0..E-1 is no expert's: in no pass.
-template <int CP>
+constexpr int kKeyBits = 7;  // an assignment's key: expert, then index
+static_assert(kMaxRows == 1 << kKeyBits, "keys");
+
+// Number of passes. An id outside 0..E-1 is no expert's: in no pass. An
+// assignment's rank is the number of smaller keys; the threads share the
+// comparisons, W / 2 of them for each assignment.
+template <int CP, int W>
 __device__ __forceinline__ int build_passes(Passes& p, const Int4Args& a)
 {
     const int tid = threadIdx.x, A = a.T * a.k;
+    const uint32_t pitch = (uint32_t)a.K * 2;
     if (!a.ids) {
         if (tid < A)
-            p.order[tid] = (int16_t)tid;
-        if (tid * CP < A) {
-            p.start[tid] = (int16_t)(tid * CP);
-            p.count[tid] = (int16_t)min(CP, A - tid * CP);
-            p.expert[tid] = 0;
-        }
+            p.row[tid] = Row{(uint32_t)tid * pitch, (int16_t)tid, (int16_t)tid, 0.0f, 0u};
+        if (tid * CP < A)
+            p.pass[tid] = Pass{0, (int16_t)(tid * CP), (int16_t)min(CP, A - tid * CP), 0};
+        if (tid == 0)
+            p.none = 0;
         __syncthreads();
         return (A + CP - 1) / CP;
     }
+    int e = a.E + 1;  // behind the last assignment
+    float weight = 0.0f;
+    if (tid < A) {
+        const int id = a.ids[tid];
+        if (a.w)
+            weight = a.w[tid];
+        e = (uint32_t)id < (uint32_t)a.E ? id : a.E;
+    }
+    if (tid < kMaxRows) {
+        p.key[tid] = (e << kKeyBits) | tid;
+        p.counts[tid] = 0;
+    }
     if (tid < kMaxRows / 32)
         p.mask[tid] = 0;
-    int e = a.E;
-    if (tid < A) {
-        e = a.ids[tid];
-        e = e < 0 || e >= a.E ? a.E : e;
-        p.id[tid] = e;
+    if (tid == 0)
+        p.none = p.twins = 0;
+    __syncthreads();
+    if (tid < A && e == a.E)
+        p.none = 1;
+    const int mine = tid % kMaxRows;
+    if (mine < A) {
+        const int key = p.key[mine], lo = key & -kMaxRows, hi = lo + kMaxRows;
+        uint32_t n = 0;  // keys below mine, of lower experts, of experts up to mine
+        for (int b = tid / kMaxRows * 4; b < A; b += W / 2 * 4) {
+            const int4 o = *(const int4*)&p.key[b];
+            n += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+            n += ((o.x < lo) + (o.y < lo) + (o.z < lo) + (o.w < lo)) << 8;
+            n += ((o.x < hi) + (o.y < hi) + (o.z < hi) + (o.w < hi)) << 16;
+        }
+        atomicAdd(&p.counts[mine], n);
     }
     __syncthreads();
-    int below = 0, before = 0, same = 0;
+    int rank = 0, before = 0, same = 0;
+    bool starts = false;
     if (tid < A) {
-        for (int b = 0; b < A; ++b) {
-            const int o = p.id[b];
-            below += o < e;
-            same += o == e;
-            before += o == e && b < tid;
-        }
-        p.order[below + before] = (int16_t)tid;
+        const uint32_t n = p.counts[tid];
+        rank = n & 255;
+        before = rank - (int)(n >> 8 & 255);
+        same = (int)(n >> 16) - (int)(n >> 8 & 255);
+        const int t = (int)((uint32_t)tid / (uint32_t)a.k), slot = tid - t * a.k;
+        p.row[rank] = Row{(uint32_t)(a.x_per_slot ? tid : t) * pitch, (int16_t)tid, (int16_t)t, weight, 0u};
+        starts = e < a.E && before % CP == 0;
+        if (starts)
+            atomicOr(&p.mask[rank >> 5], 1u << (rank & 31));
+        for (int j = 1; j <= slot; ++j)
+            if (e < a.E && p.key[tid - j] >> kKeyBits == e)
+                p.twins = 1;
     }
-    const bool starts = tid < A && e < a.E && before % CP == 0;
-    const int rank = below + before;
-    if (starts)
-        atomicOr(&p.mask[rank >> 5], 1u << (rank & 31));
     __syncthreads();
     int n = 0, at = 0;
 #pragma unroll
@@ -159,11 +201,8 @@ __device__ __forceinline__ int build_passes(Passes& p, const Int4Args& a)
         n += __popc(m);
         at += q < (rank >> 5) ? __popc(m) : q == (rank >> 5) ? __popc(m & ((1u << (rank & 31)) - 1u)) : 0;
     }
-    if (starts) {
-        p.start[at] = (int16_t)rank;
-        p.count[at] = (int16_t)min(CP, same - before);
-        p.expert[at] = (int16_t)e;
-    }
+    if (starts)
+        p.pass[at] = Pass{(int16_t)e, (int16_t)rank, (int16_t)min(CP, same - before), 0};
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(n);
 }
@@ -184,209 +223,560 @@ __device__ __forceinline__ void store_y(const Int4Args& a, int64_t at, float v)
         ((uint16_t*)a.y)[at] = f32_to_bf16_bits(v);
 }
 
-// A work item is a pass and RT tiles of 16 rows; kw of the workgroup's W waves
-// (a power of two) share an item, the workgroup runs W / kw items side by side.
-// Weighted: the workgroup takes RT tiles and all passes, keeps every
-// assignment's sums in LDS and adds a token's at the end, in slot order.
-template <int FORM, int NT, int RT, int MG, int W>
-__global__ __launch_bounds__(W * kWave) void int4_kernel(Int4Args a, int kw)
+// A wave-uniform address in scalar registers, named as global memory (a generic
+// one would be loaded through the flat path, whose waits are for everything).
+typedef const __attribute__((address_space(1))) uint8_t* Global;
+__device__ __forceinline__ Global uniform(const uint8_t* p)
 {
-    constexpr int CP = 16 * NT;
-    constexpr int NV = RT * NT * 256;  // totals of a wave
-    __shared__ Passes ps;
-    __shared__ float red[W][NV];
-    __shared__ float res[FORM == kWeighted ? kMaxRows : 1][16 * RT];
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    return (Global)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Barrier for LDS data; loads from global memory stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What a wave holds of a unit: RT tiles of codes with their groups, NT groups of
+// RL rows of x in RL / 4 loads each.
+template <int RL, int NT, int RT, int MG>
+struct Unit {
     typedef uint32_t Meta __attribute__((ext_vector_type(MG)));
+    Vec16 c[RT], x[NT][RL / 4];
+    Meta m[RT];
+};
 
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int slot = wv / kw, part = wv % kw, slots = W / kw;
-    const int units = units_of(a.K), tiles = tiles_of(a.N, FORM == kSwiglu), groups = tiles / RT;
-    const int passes = build_passes<CP>(ps, a);
-    const int M = FORM == kSwiglu ? a.N / 2 : a.N;
-    const bf16x8 ones = as_bf16x8(Vec16{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+// Where a wave loads next: unit u of RT tiles, its codes and groups at scalar
+// addresses (32-bit offsets per lane), x rows at the offsets xo.
+template <int NT>
+struct Cursor {
+    Global c, m;
+    int u;
+    uint32_t xo[NT];
+};
 
-    // items of this workgroup: plain and SwiGLU: (pass, tiles) pairs in turn;
-    // weighted: the passes of one pair of tiles after another
-    const int total = FORM == kWeighted ? passes : passes * groups;
-    for (int own = blockIdx.x; own < (FORM == kWeighted ? groups : (total + slots - 1) / slots); own += gridDim.x) {
-        for (int first = FORM == kWeighted ? 0 : own * slots; first < (FORM == kWeighted ? total : own * slots + 1);
-             first += slots) {
-            const int item = first + slot;
-            const bool live = item < total;
-            const int pass = !live ? 0 : FORM == kWeighted ? item : item / groups;
-            const int tg = FORM == kWeighted ? own : live ? item % groups : 0;
-            const int count = ps.count[pass], start = ps.start[pass];
-            floatx4 tot[RT][NT];
+template <int NT, int MG>
+__device__ __forceinline__ void aim(Cursor<NT>& at, const Int4Args& a, int64_t tile, int units, int u)
+{
+    at.c = uniform((const uint8_t*)a.codes + (tile * units + u) * 1024);
+    at.m = uniform((const uint8_t*)a.meta + (tile * units + u) * (64 * MG));
+    at.u = u;
+}
+
+// x as a buffer: loads past its end give zeros and touch no memory; a lane
+// without a row gets such an offset.
+constexpr uint32_t kNoRow = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t x_buffer(const Int4Args& a)
+{
+    const uint32_t rows = (uint32_t)(a.x_per_slot ? a.T * a.k : a.T);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(rows * (uint32_t)a.K * 2), 0x00020000);
+}
+
+// Loads unit at.u + j (behind the tile's last unit that one again, times a scale
+// of 0). A load of x takes 64 lanes x 16 bytes whatever the rows are, and
+// at 16 rows the four steps' loads cost more than the codes; with RL = 4 (8)
+// rows one load holds all four (two) steps, lanes l%16 = RL i + row those of the
+// i-th, and row_rotate brings a step to lanes 0..RL-1 of each 16 (7 tokens on 8
+// experts, down: 62 -> XX us). Unconditional, also behind the row (K % 128: its
+// end again, times a scale of 0), so that waits count exactly.
+template <int RL, int NT, int RT, int MG>
+__device__ __forceinline__ void load_unit(Unit<RL, NT, RT, MG>& v, const Int4Args& a, __amdgpu_buffer_rsrc_t xb,
+                                          const Cursor<NT>& at, int units, int j)
+{
+    typedef const __attribute__((address_space(1))) Vec16* Codes;
+    typedef const __attribute__((address_space(1))) typename Unit<RL, NT, RT, MG>::Meta* Metas;
+    const uint32_t lane = threadIdx.x % kWave, co = lane * 16, mo = (lane & 15) * 4 * MG;
+    const int u = min(at.u + j, units - 1), d = u - at.u;
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    tot[r][n] = zero;
-            if (live) {
-                const int64_t tile0 = (int64_t)ps.expert[pass] * tiles + tg * RT;
-                const Vec16* wc = (const Vec16*)a.codes + tile0 * units * kWave + lane;
-                const Meta* wm = (const Meta*)a.meta + tile0 * units * 16 + (lane & 15);
-                const uint16_t* xr[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int at = ps.order[start + min(n * 16 + (lane & 15), count - 1)];
-                    xr[n] = (const uint16_t*)a.x + (int64_t)(a.x_per_slot ? at : at / a.k) * a.K + (lane >> 4) * 8;
-                }
-                for (int u = part; u < units; u += kw) {
-                    Vec16 c[RT], x[NT][4];
-                    Meta m[RT];
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        c[r] = __builtin_nontemporal_load(wc + ((int64_t)r * units + u) * kWave);
-                        m[r] = wm[((int64_t)r * units + u) * 16];
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            // behind the row (K % 128): any of it, times a scale of 0, with x as 0
-                            const int k = u * kUnitK + 32 * s;
-                            x[n][s] = *(const Vec16*)(xr[n] + min(k, a.K - 32));
-                            if (k >= a.K)
-                                x[n][s] = Vec16{0u, 0u, 0u, 0u};
-                        }
-#pragma unroll
-                    for (int g = 0; g < MG; ++g) {
-                        floatx4 acc[RT][NT], sum[NT];
-#pragma unroll
-                        for (int s4 = 0; s4 < 4 / MG; ++s4) {
-                            const int s = g * (4 / MG) + s4;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[n][s]), ones,
-                                                                                s4 ? sum[n] : zero, 0, 0, 0);
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const bf16x8 q = codes8(c[r][s]);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                        as_bf16x8(x[n][s]), q, s4 ? acc[r][n] : zero, 0, 0, 0);
-                            }
-                        }
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            uint32_t w;
-                            if constexpr (MG == 1)
-                                w = m[r][0];
-                            else
-                                w = m[r][g];
-                            const float z = __uint_as_float(w & 0xFFFF0000u);
-                            const float s = a.scales_f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)w)
-                                                         : __uint_as_float(w << 16);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    tot[r][n][i] = fmaf(s, fmaf(-z, sum[n][i], acc[r][n][i]), tot[r][n][i]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        red[wv][(r * NT + n) * 256 + i * kWave + lane] = tot[r][n][i];
-            __syncthreads();
-            // value v of a tile: x row 16 n + 4 (l / 16) + i, weight row l % 16
-            auto added = [&](int r, int v) {
-                float s = red[slot * kw][r * NT * 256 + v];
-                for (int w = 1; w < kw; ++w)
-                    s += red[slot * kw + w][r * NT * 256 + v];
-                return s;
-            };
-            if (live)
-                for (int v = part * kWave + lane; v < NT * 256; v += kw * kWave) {
-                    const int row = (v >> 8) * 16 + ((v & 63) >> 4) * 4 + ((v >> 6) & 3), col = v & 15;
-                    if (row >= count)
-                        continue;
-                    const int at = ps.order[start + row];
-                    if constexpr (FORM == kSwiglu) {
-                        const int n = tg * 16 + col;
-                        if (n < M)
-                            store_y(a, (int64_t)at * M + n, silu_f32(added(0, v)) * added(1, v));
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const int n = (tg * RT + r) * 16 + col;
-                            if constexpr (FORM == kWeighted)
-                                res[at][r * 16 + col] = added(r, v);
-                            else if (n < M)
-                                store_y(a, (int64_t)at * M + n, added(r, v));
-                        }
-                    }
-                }
-            __syncthreads();
-        }
-        if constexpr (FORM == kWeighted) {
-            for (int v = tid; v < a.T * 16 * RT; v += W * kWave) {
-                const int t = v / (16 * RT), n = own * RT * 16 + v % (16 * RT);
-                if (n >= M)
-                    continue;
-                float s = 0.0f;
-                for (int j = 0; j < a.k; ++j) {
-                    const int at = t * a.k + j;
-                    if ((uint32_t)ps.id[at] < (uint32_t)a.E)
-                        s = fmaf(a.w[at], res[at][v % (16 * RT)], s);
-                }
-                store_y(a, (int64_t)t * M + n, s);
-            }
-            __syncthreads();  // res is written again
-        }
+    for (int r = 0; r < RT; ++r) {
+        v.c[r] = __builtin_nontemporal_load((Codes)(at.c + ((int64_t)r * units + d) * 1024 + co));
+        v.m[r] = *(Metas)(at.m + ((int64_t)r * units + d) * (64 * MG) + mo);
     }
-    // assignments of no expert: rows of zeros
-    if constexpr (FORM != kWeighted) {
-        if (a.ids)
-            for (int at = 0; at < a.T * a.k; ++at)
-                if (ps.id[at] >= a.E)
-                    for (int n = blockIdx.x * W * kWave + tid; n < M; n += gridDim.x * W * kWave)
-                        store_y(a, (int64_t)at * M + n, 0.0f);
+#pragma unroll
+    for (int i = 0; i < RL / 4; ++i) {
+        if constexpr (RL == 16) {
+            const int k = min(u * kUnitK + 32 * i, a.K - 32) * 2;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                v.x[n][i] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(xb, (int)at.xo[n], k, 0));
+        } else {
+            const int k = min(u * kUnitK + 32 * (i * (16 / RL) + (int)(lane & 15) / RL), a.K - 32) * 2;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                v.x[n][i] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(xb, (int)at.xo[n] + k, 0, 0));
+        }
     }
 }
 
-template <int FORM, int NT, int RT, int W>
-hipError_t launch(const Int4Args& a, int cus, hipStream_t s)
+// Lane i of each 16 gets lane (i + N) % 16's.
+template <int N>
+__device__ __forceinline__ Vec16 row_rotate(const Vec16& v)
 {
-    const int units = units_of(a.K), groups = tiles_of(a.N, FORM == kSwiglu) / RT, A = a.T * a.k;
-    int kw = 1;
-    while (kw * 2 <= W && kw * 2 <= units)
-        kw *= 2;
-    // at most: every expert's passes
-    const int64_t passes = a.ids ? std::min(a.E, A) + A / (16 * NT) : (A + 16 * NT - 1) / (16 * NT);
-    const int64_t items = FORM == kWeighted ? groups : (passes * groups + W / kw - 1) / (W / kw);
-    const unsigned grid = (unsigned)std::min<int64_t>(items, (int64_t)cus * (W == 4 ? 8 : 2));
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(W * kWave), 0, s, a, kw); };
-    switch (unit_groups(a.group)) {
+    if constexpr (N == 0) {
+        return v;
+    } else {
+        Vec16 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // row_ror: lane i from lane i - (16 - N)
+            o[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], 0x120 + 16 - N, 0xF, 0xF, false);
+        return o;
+    }
+}
+
+// The x fragment of step S.
+template <int RL, int S>
+__device__ __forceinline__ bf16x8 x_step(const Vec16 (&x)[RL / 4])
+{
+    constexpr int per = 16 / RL;
+    return as_bf16x8(row_rotate<RL % 16 * (S % per)>(x[S / per]));
+}
+
+struct Consts {
+    uint32_t fields, sixteen;  // as codes8 takes them, in vector registers
+    uint32_t f16;              // all ones: the scales are fp16
+    __device__ __forceinline__ explicit Consts(const Int4Args& a)
+        : fields(0x00780078u), sixteen(0x41804180u), f16(a.scales_f16 ? ~0u : 0u)
+    {
+        asm volatile("" : "+v"(fields), "+v"(sixteen));
+    }
+};
+
+// tot += s * sum (q - z) x over the unit's groups (live 0: times 0 instead). A
+// group's sums are done with before the next one's begin, and the set before it
+// is loaded again: fewer registers, and no copies of what is in flight.
+template <int RL, int NT, int RT, int MG>
+__device__ __forceinline__ void multiply_unit(const Unit<RL, NT, RT, MG>& v, const Consts& k, floatx4 (&tot)[RT][NT],
+                                              uint32_t live)
+{
+    const bf16x8 ones = as_bf16x8(Vec16{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    floatx4 acc[RT][NT], sum[NT];
+    auto step = [&](auto sc) {
+        constexpr int S = decltype(sc)::value;
+        constexpr bool begins = S % (4 / MG) == 0, ends = S % (4 / MG) == 4 / MG - 1;
+        bf16x8 x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            x[n] = x_step<RL, S>(v.x[n]);
+            sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[n], ones, begins ? zero : sum[n], 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const bf16x8 q = codes8(v.c[r][S], k.fields, k.sixteen);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[n], q, begins ? zero : acc[r][n], 0, 0, 0);
+        }
+        if constexpr (ends) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const uint32_t w = v.m[r][S / (4 / MG)];
+                const float z = __uint_as_float(w & 0xFFFF0000u);
+                // the scale of either type by a bit select: no branch between the loads
+                const uint32_t half = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)w));
+                const float s = __uint_as_float(((half & k.f16) | ((w << 16) & ~k.f16)) & live);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tot[r][n][i] = fmaf(s, fmaf(-z, sum[n][i], acc[r][n][i]), tot[r][n][i]);
+                    asm volatile("" : "+v"(tot[r][n]));
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    step(std::integral_constant<int, 0>());
+    step(std::integral_constant<int, 1>());
+    step(std::integral_constant<int, 2>());
+    step(std::integral_constant<int, 3>());
+}
+
+template <int NT, int RT>
+__device__ __forceinline__ void clear(floatx4 (&tot)[RT][NT])
+{
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            tot[r][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Lane l's element i of a tile's totals: x row 16 n + 4 (l / 16) + i, weight row l % 16.
+template <int NT, int RT>
+__device__ __forceinline__ void store_totals(float* red, const floatx4 (&tot)[RT][NT])
+{
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[(r * NT + n) * 256 + i * kWave + lane] = tot[r][n][i];
+}
+
+// x row and weight row of value v of a tile's totals.
+__device__ __forceinline__ int total_row(int v) { return (v >> 8) * 16 + ((v & 63) >> 4) * 4 + ((v >> 6) & 3); }
+__device__ __forceinline__ int total_col(int v) { return v & 15; }
+
+// Plain and SwiGLU. A work item is a pass and RT tiles of 16 rows. A workgroup
+// takes a contiguous share of the items; of these every wave takes whole ones, one
+// after another, and stores them itself, as long as there are W more. The units
+// of the rest are one line, cut into W pieces: a piece is part of two items at
+// most, and what the waves summed of an item is added through LDS, in wave order.
+// So all waves stream all the time, and meet once. Units go by Q in a turn (the
+// last ones past the row count for nothing): as the products of one are done,
+// the same one of the next turn is loaded.
+template <bool SWIGLU, int RL, int NT, int RT, int MG, int W, int Q>
+__global__ __launch_bounds__(W * kWave) void int4_kernel(Int4Args a)
+{
+    static_assert(NT == 1 || RL == 16, "rows");
+    constexpr int CP = RL * NT, NV = RT * NT * 256;
+    __shared__ Passes ps;
+    __shared__ int first_item[W];
+    __shared__ float red[W][2][NV];
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int units = units_of(a.K), turns = (units + Q - 1) / Q, tiles = tiles_of(a.N, SWIGLU), groups = tiles / RT;
+    const uint32_t items = (uint32_t)(build_passes<CP, W>(ps, a) * groups);
+    const int M = SWIGLU ? a.N / 2 : a.N;
+    const Consts consts(a);
+    const __amdgpu_buffer_rsrc_t xb = x_buffer(a);
+
+    const uint32_t share = items / gridDim.x, more = items % gridDim.x;
+    const int mine = (int)(share + (blockIdx.x < more ? 1 : 0));
+    const int i0 = (int)(blockIdx.x * share + min(blockIdx.x, more));
+    const int full = mine / W, rest = mine % W, rest0 = i0 + full * W;
+    const uint32_t line = (uint32_t)(rest * turns);
+    const int cut0 = (int)(line * wv / W), cut1 = (int)(line * (wv + 1) / W);  // this wave's piece
+    const int first = (int)((uint32_t)cut0 / (uint32_t)turns);               // its first item of the rest
+    const int segments = full + (cut1 > cut0) + (cut1 > (first + 1) * turns);
+    if (lane == 0)
+        first_item[wv] = first;
+    struct Segment {
+        int item, q0, q1;
+    };
+    auto segment = [&](int k) {
+        if (k < full)
+            return Segment{i0 + k * W + wv, 0, turns};
+        const int m = first + k - full;
+        return Segment{rest0 + m, max(cut0 - m * turns, 0), min(cut1 - m * turns, turns)};
+    };
+
+    // The load cursor. Past the last segment it stays where it is.
+    Cursor<NT> at;
+    int lk = 0, lend = 0;
+    auto aim_at = [&]() {
+        const Segment s = segment(lk);
+        const int pass = (int)((uint32_t)s.item / (uint32_t)groups), tg = s.item - pass * groups;
+        const Pass p = ps.pass[pass];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = n * 16 + (lane % RL);
+            at.xo[n] = row >= p.count ? kNoRow : ps.row[p.start + row].x + (lane >> 4) * 16;
+        }
+        aim<NT, MG>(at, a, (int64_t)__builtin_amdgcn_readfirstlane((int)p.expert) * tiles + tg * RT, units, s.q0 * Q);
+        lend = s.q1 * Q;
+    };
+    auto advance = [&]() {
+        if (at.u + Q < lend) {
+            at.u += Q;
+            at.c += Q * 1024;
+            at.m += Q * 64 * MG;
+        } else if (lk + 1 < segments) {
+            ++lk;
+            aim_at();
+        }
+    };
+    // Row `row` of a pass, weight rows col of the item's RT tiles: sums v[r].
+    auto store = [&](int pass, int tg, int row, int col, const float (&v)[RT]) {
+        const Pass p = ps.pass[pass];
+        if (row >= p.count)
+            return;
+        const int64_t y = (int64_t)ps.row[p.start + row].assigned * M;
+        if constexpr (SWIGLU) {
+            const int n = tg * 16 + col;
+            if (n < M)
+                store_y(a, y + n, silu_f32(v[0]) * v[1]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int n = (tg * RT + r) * 16 + col;
+                if (n < M)
+                    store_y(a, y + n, v[r]);
+            }
+        }
+    };
+
+    if (segments > 0) {
+        aim_at();
+        Unit<RL, NT, RT, MG> v[Q];
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            load_unit(v[j], a, xb, at, units, j);
+            __builtin_amdgcn_sched_barrier(0);  // in this order, for the waits in the loop
+        }
+        floatx4 tot[RT][NT];
+        clear(tot);
+        int k = 0;
+        Segment now = segment(0);
+        for (;;) {
+            advance();
+#pragma unroll
+            for (int j = 0; j < Q; ++j) {
+                multiply_unit(v[j], consts, tot, j == 0 || now.q0 * Q + j < units ? ~0u : 0u);
+                load_unit(v[j], a, xb, at, units, j);
+            }
+            if (++now.q0 < now.q1)
+                continue;
+            if (k < full) {
+                const int pass = (int)((uint32_t)now.item / (uint32_t)groups), tg = now.item - pass * groups;
+#pragma unroll 1
+                for (int t = 0; t < NT; ++t)
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        float w[RT];
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            w[r] = NT == 1 ? tot[r][0][i] : tot[r][t][i];
+                        store(pass, tg, t * 16 + (lane >> 4) * 4 + i, lane & 15, w);
+                    }
+            } else {
+                store_totals(red[wv][k - full], tot);
+            }
+            clear(tot);
+            if (++k == segments)
+                break;
+            now = segment(k);
+        }
+    }
+    if (rest > 0) {
+        lds_barrier();
+        const int firsts = first_item[lane % W];
+        for (int i = tid; i < rest * NT * 256; i += W * kWave) {
+            const int m = __builtin_amdgcn_readfirstlane(i / (NT * 256)), v = i % (NT * 256);
+            float sum[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                sum[r] = 0.0f;
+#pragma unroll 1
+            for (int w0 = 0; w0 < W; w0 += 4) {  // the waves with a piece of item m, in order
+                float p[4][RT];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int w = w0 + j, c0 = (int)(line * w / W), c1 = (int)(line * (w + 1) / W);
+                    const bool has = c0 < c1 && c0 < (m + 1) * turns && c1 > m * turns;
+                    const float* t = &red[w][has ? m - __builtin_amdgcn_readlane(firsts, w) : 0][v];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        p[j][r] = has ? t[r * NT * 256] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        sum[r] += p[j][r];
+            }
+            const int pass = (int)((uint32_t)(rest0 + m) / (uint32_t)groups);
+            store(pass, rest0 + m - pass * groups, total_row(v), total_col(v), sum);
+        }
+    }
+    if (ps.none)  // assignments of no expert: rows of zeros
+        for (int p = 0; p < a.T * a.k; ++p)
+            if (ps.key[p] >> kKeyBits == a.E)
+                for (int n = blockIdx.x * W * kWave + tid; n < M; n += gridDim.x * W * kWave)
+                    store_y(a, (int64_t)p * M + n, 0.0f);
+}
+
+// y[t] = sum_j w[t][j] W[ids[t][j]] x. A workgroup takes RT tiles and all tokens;
+// the units of all passes are one line, cut into W pieces, one per wave. At the
+// end of a pass, or of its piece, a wave adds w times what it summed to its own
+// sums of the tokens in LDS, and these are added once, in wave order.
+template <int RL, int RT, int MG, int W, int Q>
+__global__ __launch_bounds__(W * kWave) void int4_sum_kernel(Int4Args a)
+{
+    __shared__ Passes ps;
+    extern __shared__ float sums[];  // [W][T][16 RT]
+    constexpr int C = 16 * RT;
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int units = units_of(a.K), turns = (units + Q - 1) / Q, tiles = tiles_of(a.N, 0);
+    const int tg = blockIdx.x;
+    for (int i = tid; i < W * a.T * C; i += W * kWave)
+        sums[i] = 0.0f;
+    const uint32_t line = (uint32_t)(build_passes<RL, W>(ps, a) * turns);
+    const int cut0 = (int)(line * wv / W), cut1 = (int)(line * (wv + 1) / W);
+    const Consts consts(a);
+    const __amdgpu_buffer_rsrc_t xb = x_buffer(a);
+
+    if (cut1 > cut0) {
+        // The load cursor: `left` turns to the end of the piece, where it stays.
+        Cursor<1> at;
+        int lp = (int)((uint32_t)cut0 / (uint32_t)turns), left = cut1 - cut0;
+        auto aim_at = [&](int q) {
+            const Pass p = ps.pass[lp];
+            at.xo[0] = lane % RL >= p.count ? kNoRow : ps.row[p.start + lane % RL].x + (lane >> 4) * 16;
+            aim<1, MG>(at, a, (int64_t)__builtin_amdgcn_readfirstlane((int)p.expert) * tiles + tg * RT, units, q * Q);
+        };
+        auto advance = [&]() {
+            if (--left <= 0)
+                return;
+            if (at.u + Q < units) {
+                at.u += Q;
+                at.c += Q * 1024;
+                at.m += Q * 64 * MG;
+            } else {
+                ++lp;
+                aim_at(0);
+            }
+        };
+        int p = lp, q = cut0 - p * turns, todo = cut1 - cut0;
+        aim_at(q);
+        Unit<RL, 1, RT, MG> v[Q];
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            load_unit(v[j], a, xb, at, units, j);
+            __builtin_amdgcn_sched_barrier(0);  // in this order, for the waits in the loop
+        }
+        floatx4 sum[RT][1];
+        clear(sum);
+        for (;;) {
+            advance();
+#pragma unroll
+            for (int j = 0; j < Q; ++j) {
+                multiply_unit(v[j], consts, sum, j == 0 || q * Q + j < units ? ~0u : 0u);
+                load_unit(v[j], a, xb, at, units, j);
+            }
+            if (++q < turns && --todo > 0)
+                continue;
+            // a token has one row in a pass, unless it has the expert twice: then
+            // the lane groups take turns
+            const Pass now = ps.pass[p];
+            const int groups = ps.twins ? 4 : 1;
+#pragma unroll 1
+            for (int g = 0; g < groups; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (lane >> 4) * 4 + i;
+                    if (row < now.count && (groups == 1 || (lane >> 4) == g)) {
+                        const Row o = ps.row[now.start + row];
+                        float* y = sums + (wv * a.T + o.token) * C + (lane & 15);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            y[r * 16] = fmaf(o.w, sum[r][0][i], y[r * 16]);
+                    }
+                }
+            clear(sum);
+            if (q == turns) {
+                q = 0;
+                ++p;
+                if (--todo <= 0)
+                    break;
+            } else {
+                break;
+            }
+        }
+    }
+    lds_barrier();
+    for (int v = tid; v < a.T * C; v += W * kWave) {
+        const int n = tg * C + v % C;
+        float s = sums[v];
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+            s += sums[w * a.T * C + v];
+        if (n < a.N)
+            store_y(a, (int64_t)(v / C) * a.N + n, s);
+    }
+}
+
+// go(MG): with the number of groups of a unit at compile time.
+template <class Go>
+hipError_t by_groups(int group, Go go)
+{
+    switch (unit_groups(group)) {
     case 4:
-        go(int4_kernel<FORM, NT, RT, 4, W>);
+        go(std::integral_constant<int, 4>());
         break;
     case 2:
-        go(int4_kernel<FORM, NT, RT, 2, W>);
+        go(std::integral_constant<int, 2>());
         break;
     default:
-        go(int4_kernel<FORM, NT, RT, 1, W>);
+        go(std::integral_constant<int, 1>());
     }
     return hipGetLastError();
 }
 
-template <int NT>
-hipError_t launch_form(const Int4Args& a, int cus, hipStream_t s)
+template <bool SWIGLU, int RL, int NT, int RT, int W, int Q = 2>
+hipError_t launch(const Int4Args& a, int per_cu, int cus, hipStream_t s)
 {
-    if (a.swiglu)
-        return launch<kSwiglu, NT, 2, 4>(a, cus, s);
-    if (a.w)
-        return launch<kWeighted, NT, 2, NT == 1 ? 16 : 8>(a, cus, s);
-    return launch<kPlain, NT, 2, 4>(a, cus, s);
+    const int groups = tiles_of(a.N, SWIGLU) / RT, A = a.T * a.k, CP = RL * NT;
+    // at most: every expert's passes
+    const int64_t passes = a.ids ? std::min(a.E, A) + A / CP : (A + CP - 1) / CP;
+    const unsigned grid = (unsigned)std::min<int64_t>(passes * groups, (int64_t)cus * per_cu);
+    return by_groups(a.group, [&](auto mg) {
+        hipLaunchKernelGGL((int4_kernel<SWIGLU, RL, NT, RT, decltype(mg)::value, W, Q>), dim3(grid), dim3(W * kWave), 0, s, a);
+    });
+}
+
+template <int RL, int RT, int Q>
+hipError_t launch_sum(const Int4Args& a, hipStream_t s)
+{
+    constexpr int W = 16;
+    const unsigned grid = (unsigned)(tiles_of(a.N, 0) / RT);
+    const size_t lds = (size_t)W * a.T * 16 * RT * sizeof(float);
+    return by_groups(a.group, [&](auto mg) {
+        hipLaunchKernelGGL((int4_sum_kernel<RL, RT, decltype(mg)::value, W, Q>), dim3(grid), dim3(W * kWave), lds, s, a);
+    });
+}
+
+// Two tiles per workgroup where that leaves one for every compute unit and the
+// sums of the tokens fit (N = 8192: 36.7 -> 27.7 us; with too few, N = 4096, 53 ->
+// 67). Four units in a turn for long rows (K = 14336: 53 -> 49 us; K = 2048: 8.6 ->
+// 9.8).
+template <int RL>
+hipError_t launch_sums(const Int4Args& a, int cus, hipStream_t s)
+{
+    if (tiles_of(a.N, 0) / 2 >= cus && a.T <= 64)
+        return launch_sum<RL, 2, 2>(a, s);
+    if constexpr (RL < 16) {
+        if (a.K >= 8192)
+            return launch_sum<RL, 1, 4>(a, s);
+    }
+    return launch_sum<RL, 1, 2>(a, s);
+}
+
+// Many items: four workgroups of four waves per compute unit, whose starts and
+// ends overlap the others' streaming (16 tokens over 128 experts of 1536 x 2048:
+// 23.3 us, two of eight waves 24.7, one of sixteen 28; 8 experts of 28672 x 4096, one
+// token: 26.5, 29.6, 31.6). Few: eight waves for an item (one token, 4096 x 4096: 5.8
+// us, 6.5 with four; K = 14336: 10.8, 14.2).
+template <int RL, int NT>
+hipError_t launch_items(const Int4Args& a, int cus, hipStream_t s)
+{
+    const int A = a.T * a.k, CP = RL * NT;
+    const int64_t passes = a.ids ? std::min(a.E, A) : (A + CP - 1) / CP;
+    const int64_t tiles = passes * tiles_of(a.N, a.swiglu);
+    if constexpr (NT == 1) {
+        if (a.swiglu)
+            return tiles / 2 >= 2 * cus ? launch<true, RL, 1, 2, 4>(a, 4, cus, s) : launch<true, RL, 1, 2, 8>(a, 2, cus, s);
+        if (tiles / 2 >= 2 * cus)
+            return launch<false, RL, 1, 2, 4>(a, 4, cus, s);
+        return tiles >= 2 * cus ? launch<false, RL, 1, 1, 4>(a, 4, cus, s) : launch<false, RL, 1, 1, 8>(a, 2, cus, s);
+    } else {
+        if (a.swiglu)
+            return launch<true, 16, NT, 2, 4, 1>(a, 2, cus, s);
+        if (tiles / 2 >= 2 * cus)
+            return launch<false, 16, NT, 2, 4, 1>(a, 2, cus, s);
+        return launch<false, 16, NT, 1, 4, 1>(a, 3, cus, s);
+    }
 }
 
 }  // namespace
@@ -410,13 +800,24 @@ hipError_t launch_int4_pack(const Int4Pack& p, hipStream_t s)
 
 hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s)
 {
-    // x rows of a pass: one group of 16 while an expert has few of them
-    const int rows = !a.ids ? a.T : a.T <= 16 ? 1 : 2 * a.T * a.k / a.E;
-    if (rows <= 16)
-        return launch_form<1>(a, cus, s);
-    if (rows <= 32)
-        return launch_form<2>(a, cus, s);
-    return launch_form<4>(a, cus, s);
+    const int A = a.T * a.k;
+    // The rows that passes hold: with ids, the mean of the chosen experts' (if all
+    // choose alike), in eighths. Fewer rows per pass make loads of x cheaper, but
+    // an expert of more is read again: passes of 4 up to 1.6 rows, of 8 up to 4.5 (16
+    // tokens on 8 experts, 4 rows each: 8 rows 91.6 us, 4 rows 122, 16 rows 91.8).
+    const int rows = !a.ids ? a.T * 8 : a.T <= 4 ? 8 : std::min(a.T * 8, A * 8 / std::min(a.E, A));
+    if (a.w) {
+        if (rows <= 13)
+            return launch_sums<4>(a, cus, s);
+        return rows <= 36 ? launch_sums<8>(a, cus, s) : launch_sums<16>(a, cus, s);
+    }
+    if (rows <= (a.ids ? 13 : 32))
+        return launch_items<4, 1>(a, cus, s);
+    if (rows <= (a.ids ? 36 : 64))
+        return launch_items<8, 1>(a, cus, s);
+    if (rows <= 128)
+        return launch_items<16, 1>(a, cus, s);
+    return rows <= 256 ? launch_items<16, 2>(a, cus, s) : launch_items<16, 4>(a, cus, s);
 }
 
 }  // namespace cmoe
