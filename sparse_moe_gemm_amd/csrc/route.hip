@@ -11,35 +11,51 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float logit_of(const float* p) { return *p; }
-__device__ __forceinline__ float logit_of(const uint16_t* p) { return bf16_to_f32(*p); }
+// A token's logits in memory.
+template <typename T, bool VEC>
+struct RowLogits {
+    const T* row;
+    int E;
+    __device__ __forceinline__ float one(int e) const { return element(row, e); }
+    template <int NQ>
+    __device__ __forceinline__ void all(int e0, float (&l)[NQ]) const
+    {
+        load_row<VEC>(row, e0, E, -INFINITY, l);
+    }
+};
 
-// One wave per token.
-template <typename T, int NQ>
+template <typename T, bool VEC, int NQ>
 __global__ __launch_bounds__(kThreads) void route_kernel(const T* logits, int64_t ld, int tokens, int E, int k,
                                                          SelectRule rule, int32_t* ids, float* w)
 {
-    const int waves = (int)gridDim.x * (kThreads / kWave);
-    for (int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; t < tokens; t += waves) {
-        const T* row = logits + t * ld;
-        select_token<NQ>([&](int e) { return logit_of(row + e); }, E, k, rule, ids + t * k, w + t * k);
-    }
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / kRow) + threadIdx.x / kRow;
+    select_token<NQ>(RowLogits<T, VEC>{logits + min(t, (int64_t)tokens - 1) * ld, E}, E, k, rule, t < tokens, ids + t * k,
+                     w + t * k);
 }
 
 template <typename T>
 hipError_t launch(const RouteArgs& a, hipStream_t s)
 {
-    const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)a.T + 3) / 4, 8192);
+    constexpr int kRows = kThreads / kRow;
+    constexpr int64_t kMost = 1 << 27;  // tokens of a launch, which has fewer than 2^32 threads
     auto go = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3(blocks), dim3(kThreads), 0, s, (const T*)a.logits, a.ld, a.T, a.E, a.k, a.rule,
-                           a.ids, a.w);
+        for (int64_t t = 0; t < a.T; t += kMost) {
+            const int n = (int)std::min<int64_t>(a.T - t, kMost);
+            hipLaunchKernelGGL(kern, dim3((unsigned)((n + kRows - 1) / kRows)), dim3(kThreads), 0, s,
+                               (const T*)a.logits + t * a.ld, a.ld, n, a.E, a.k, a.rule, a.ids + t * a.k, a.w + t * a.k);
+        }
     };
-    if (a.E <= 64)
-        go(route_kernel<T, 1>);
-    else if (a.E <= 128)
-        go(route_kernel<T, 2>);
-    else
-        go(route_kernel<T, 4>);
+    auto width = [&](auto nq) {
+        if (((uintptr_t)a.logits & 15u) == 0 && a.ld * sizeof(T) % 16 == 0)  // every row
+            go(route_kernel<T, true, nq()>);
+        else
+            go(route_kernel<T, false, nq()>);
+    };
+    switch (select_width(a.E)) {
+    case 4: width(std::integral_constant<int, 4>{}); break;
+    case 8: width(std::integral_constant<int, 8>{}); break;
+    default: width(std::integral_constant<int, 16>{}); break;
+    }
     return hipGetLastError();
 }
 

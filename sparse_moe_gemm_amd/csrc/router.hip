@@ -147,7 +147,7 @@ __global__ __launch_bounds__(W * kWave) void router_bf16_kernel(RouterArgs a)
     __syncthreads();
     store_logits(&part[0][0], LDL, BT, t0, a.T, a.E, a.logits);
     if constexpr (RULE)
-        select_epilogue<(EP + kWave - 1) / kWave>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
+        select_epilogue<select_width(EP)>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
     else
         topk_softmax_epilogue<(EP + kWave - 1) / kWave>(&part[0][0], LDL, BT, t0, a.T, a.E, a.k, a.ids, a.w);
 }
@@ -171,9 +171,16 @@ __global__ __launch_bounds__(kThreads) void router_f32_kernel(RouterArgs a)
     }
     __syncthreads();
     store_logits(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.logits);
-    if constexpr (RULE)
-        select_epilogue<kMaxExperts / kWave>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
-    else
+    if constexpr (RULE) {
+        auto select = [&](auto nq) {
+            select_epilogue<nq()>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.rule, a.ids, a.w);
+        };
+        switch (select_width(a.E)) {
+        case 4: select(std::integral_constant<int, 4>{}); break;
+        case 8: select(std::integral_constant<int, 8>{}); break;
+        default: select(std::integral_constant<int, 16>{}); break;
+        }
+    } else
         topk_softmax_epilogue<kMaxExperts / kWave>(&lg[0][0], kMaxExperts + 1, kTok, t0, a.T, a.E, a.k, a.ids, a.w);
 }
 

@@ -4,9 +4,10 @@ out. Also which tokens the library's fp32 may decide differently.
 
 Error of a kernel's score (in steps of 2^-24, relative): the exponential of a
 correctly rounded difference d is off by |d| + 2, 1 + exp and its reciprocal
-by 2, a softmax's sum over at most 256 terms (at most 3 additions in a lane, 6
-across the wave, each term off as above) and the division by 9 + 3 + |d_max|;
-a weight adds its own sum of at most 8 terms, a division and the scale: 10.
+by 2, a softmax's sum over at most 256 terms (4 levels of additions in a lane,
+4 across its row, each term off as above), its reciprocal and the product by
+8 + 4 + |d_max|; a weight adds its own sum of at most 8 terms, a division and
+the scale: 10.
 Scores are therefore within (2 |d|max + 32) * 2^-24, weights within twice that."""
 from __future__ import annotations
 
