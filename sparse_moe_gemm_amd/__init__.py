@@ -418,15 +418,20 @@ class Normed(NamedTuple):
     scales: object
 
 
-def _rows_of(t, like, name):
-    """Row stride of a 2-D device tensor that fits `like`."""
-    if t.dtype != like.dtype or tuple(t.shape) != tuple(like.shape) or t.device != like.device:
-        raise TypeError(f"{name} must have the shape, dtype and device of x")
+def _row_stride(t, name):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
     rows, cols = t.shape
     stride, step = t.stride()
     if (cols > 1 and step != 1) or (rows > 1 and stride < cols):
         raise ValueError(f"rows of {name} must be contiguous and must not overlap")
     return stride if rows > 1 else cols
+
+
+def _rows_of(t, like, name):
+    """Row stride of a 2-D device tensor that fits `like`."""
+    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+        raise TypeError(f"{name} must have the shape, dtype and device of x")
+    return _row_stride(t, name)
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=None, residual_out=None, stream=None):
@@ -446,14 +451,15 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
     if not (bf16 or x.dtype == torch.float32) or x.dim() != 2 or not x.is_cuda:
         raise TypeError("x must be a 2-D bfloat16 or float32 device tensor")
     T, d = x.shape
-    x_stride = _rows_of(x, x, "x")
-    if weight.dtype not in (x.dtype, torch.float32) or weight.device != x.device or weight.dim() != 1:
+    x_stride = _row_stride(x, "x")
+    w_bf16 = weight.dtype == torch.bfloat16
+    if not (w_bf16 and bf16 or weight.dtype == torch.float32) or weight.device != x.device or weight.dim() != 1:
         raise TypeError("weight must be a 1-D tensor of x's dtype or float32 on x's device")
     if weight.shape[0] != d or not weight.is_contiguous():
         raise ValueError("weight must be contiguous and hold d values")
     if quantize not in (None, "fp8"):
         raise ValueError('quantize must be None or "fp8"')
-    if y is not None and (y.dtype != x.dtype or tuple(y.shape) != (T, d) or y.device != x.device
+    if y is not None and (y.dtype != x.dtype or y.shape != x.shape or y.device != x.device
                           or not y.is_contiguous()):
         raise TypeError("y must be a contiguous tensor of x's shape, dtype and device")
     r_stride = _rows_of(residual, x, "residual") if residual is not None else d
@@ -482,10 +488,10 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
     out = Normed(y, residual_out, codes, scales)
     if T == 0 or d == 0:
         return out
-    dtype = BF16 if bf16 else F32
-    p = [None if t is None else t.data_ptr() for t in (residual, y, residual_out, codes, scales)]
-    n = Norm(x.data_ptr(), x_stride, p[0], r_stride, weight.data_ptr(), dtype,
-             BF16 if weight.dtype == torch.bfloat16 else F32, T, d, eps, p[1], p[2], ro_stride, p[3], p[4])
+    n = Norm(x.data_ptr(), x_stride, None if residual is None else residual.data_ptr(), r_stride, weight.data_ptr(),
+             BF16 if bf16 else F32, BF16 if w_bf16 else F32, T, d, eps, None if y is None else y.data_ptr(),
+             None if residual is None else residual_out.data_ptr(), ro_stride,
+             None if codes is None else codes.data_ptr(), None if codes is None else scales.data_ptr())
     st = _on_device_of(x, colibri_moe_rms_norm, n, _stream_of(x, stream))
     if st != OK:
         raise ColibriError("colibri_moe_rms_norm", st)
