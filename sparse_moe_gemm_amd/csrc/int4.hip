@@ -8,9 +8,9 @@
 //   SwiGLU:   y[a][c] = SiLU(y[a][c]) * y[a][f + c]       (rows 0..f-1 gate, f..2f-1 up)
 //   weighted: y[t][n] = sum_j w[t][j] * y[t * k_slots + j][n]
 //
-// As few.hip, the work is reading the weights of the experts in use once: 16
-// weight rows are the second operand of v_mfma_f32_16x16x32_bf16, up to 16 rows
-// of x (assignments of one expert) the first.
+// As few.hip, the work is reading the weights of the experts in use once (from 16
+// rows of x on, the products): 16 weight rows are the second operand of
+// v_mfma_f32_16x16x32_bf16, 16 rows of x (assignments of one expert) the first.
 //   * A code q becomes the bf16 value 16 + q, exact, by placing its four bits in
 //     the mantissa of 16 (a shift and an and-or for two codes). The matrix unit
 //     sums (16 + q) x over a group in fp32; with the group's sum of x, from a
@@ -20,8 +20,10 @@
 //   * A unit is 16 rows x 128 k: one KiB in which lane l's 16 bytes are row l%16,
 //     k = 32 s + 8 (l/16) .. +8 for the four MFMA steps s, so that a step's 32 k
 //     lie in one group; its scales and zero points are a dword per row and group.
-//   * The waves of a work item split its units and add their totals through LDS
-//     in wave order: the result does not depend on what else runs.
+//   * The waves of a workgroup split its units and add their totals through LDS in
+//     wave order: the result does not depend on what else runs.
+// One token x 4096 x 4096: 4.2 us with the launch, of which 1.6 are the weights' 9 MB;
+// 16 tokens on 8 experts of 28672 x 4096 (SwiGLU, 4 rows each): 87 us, 5.6 TB/s.
 #include "common.hpp"
 
 namespace cmoe {
@@ -242,32 +244,6 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
-// What a wave holds of a unit: RT tiles of codes with their groups, NT groups of
-// RL rows of x in RL / 4 loads each.
-template <int RL, int NT, int RT, int MG>
-struct Unit {
-    typedef uint32_t Meta __attribute__((ext_vector_type(MG)));
-    Vec16 c[RT], x[NT][RL / 4];
-    Meta m[RT];
-};
-
-// Where a wave loads next: unit u of RT tiles, its codes and groups at scalar
-// addresses (32-bit offsets per lane), x rows at the offsets xo.
-template <int NT>
-struct Cursor {
-    Global c, m;
-    int u;
-    uint32_t xo[NT];
-};
-
-template <int NT, int MG>
-__device__ __forceinline__ void aim(Cursor<NT>& at, const Int4Args& a, int64_t tile, int units, int u)
-{
-    at.c = uniform((const uint8_t*)a.codes + (tile * units + u) * 1024);
-    at.m = uniform((const uint8_t*)a.meta + (tile * units + u) * (64 * MG));
-    at.u = u;
-}
-
 // x as a buffer: loads past its end give zeros and touch no memory; a lane
 // without a row gets such an offset.
 constexpr uint32_t kNoRow = 0x80000000u;
@@ -275,65 +251,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t x_buffer(const Int4Args& a)
 {
     const uint32_t rows = (uint32_t)(a.x_per_slot ? a.T * a.k : a.T);
     return __builtin_amdgcn_make_buffer_rsrc((void*)a.x, 0, (int)(rows * (uint32_t)a.K * 2), 0x00020000);
-}
-
-// Loads unit at.u + j (behind the tile's last unit that one again, times a scale
-// of 0). A load of x takes 64 lanes x 16 bytes whatever the rows are, and
-// at 16 rows the four steps' loads cost more than the codes; with RL = 4 (8)
-// rows one load holds all four (two) steps, lanes l%16 = RL i + row those of the
-// i-th, and row_rotate brings a step to lanes 0..RL-1 of each 16 (7 tokens on 8
-// experts, down: 62 -> XX us). Unconditional, also behind the row (K % 128: its
-// end again, times a scale of 0), so that waits count exactly.
-template <int RL, int NT, int RT, int MG>
-__device__ __forceinline__ void load_unit(Unit<RL, NT, RT, MG>& v, const Int4Args& a, __amdgpu_buffer_rsrc_t xb,
-                                          const Cursor<NT>& at, int units, int j)
-{
-    typedef const __attribute__((address_space(1))) Vec16* Codes;
-    typedef const __attribute__((address_space(1))) typename Unit<RL, NT, RT, MG>::Meta* Metas;
-    const uint32_t lane = threadIdx.x % kWave, co = lane * 16, mo = (lane & 15) * 4 * MG;
-    const int u = min(at.u + j, units - 1), d = u - at.u;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        v.c[r] = __builtin_nontemporal_load((Codes)(at.c + ((int64_t)r * units + d) * 1024 + co));
-        v.m[r] = *(Metas)(at.m + ((int64_t)r * units + d) * (64 * MG) + mo);
-    }
-#pragma unroll
-    for (int i = 0; i < RL / 4; ++i) {
-        if constexpr (RL == 16) {
-            const int k = min(u * kUnitK + 32 * i, a.K - 32) * 2;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                v.x[n][i] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(xb, (int)at.xo[n], k, 0));
-        } else {
-            const int k = min(u * kUnitK + 32 * (i * (16 / RL) + (int)(lane & 15) / RL), a.K - 32) * 2;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                v.x[n][i] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(xb, (int)at.xo[n] + k, 0, 0));
-        }
-    }
-}
-
-// Lane i of each 16 gets lane (i + N) % 16's.
-template <int N>
-__device__ __forceinline__ Vec16 row_rotate(const Vec16& v)
-{
-    if constexpr (N == 0) {
-        return v;
-    } else {
-        Vec16 o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // row_ror: lane i from lane i - (16 - N)
-            o[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], 0x120 + 16 - N, 0xF, 0xF, false);
-        return o;
-    }
-}
-
-// The x fragment of step S.
-template <int RL, int S>
-__device__ __forceinline__ bf16x8 x_step(const Vec16 (&x)[RL / 4])
-{
-    constexpr int per = 16 / RL;
-    return as_bf16x8(row_rotate<RL % 16 * (S % per)>(x[S / per]));
 }
 
 struct Consts {
@@ -346,12 +263,12 @@ struct Consts {
     }
 };
 
-// tot += s * sum (q - z) x over the unit's groups (live 0: times 0 instead). A
-// group's sums are done with before the next one's begin, and the set before it
-// is loaded again: fewer registers, and no copies of what is in flight.
-template <int RL, int NT, int RT, int MG>
-__device__ __forceinline__ void multiply_unit(const Unit<RL, NT, RT, MG>& v, const Consts& k, floatx4 (&tot)[RT][NT],
-                                              uint32_t live)
+// tot += s * sum (q - z) x over the unit's groups, the x
+// fragments from x_of(step, n). A group's sums are done with before the next
+// one's begin: fewer registers.
+template <int NT, int RT, int MG, class X, class Meta>
+__device__ __forceinline__ void multiply_unit(X x_of, const Vec16 (&c)[RT], const Meta (&m)[RT], const Consts& k,
+                                              floatx4 (&tot)[RT][NT])
 {
     const bf16x8 ones = as_bf16x8(Vec16{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -362,12 +279,12 @@ __device__ __forceinline__ void multiply_unit(const Unit<RL, NT, RT, MG>& v, con
         bf16x8 x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            x[n] = x_step<RL, S>(v.x[n]);
+            x[n] = x_of(sc, n);
             sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[n], ones, begins ? zero : sum[n], 0, 0, 0);
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const bf16x8 q = codes8(v.c[r][S], k.fields, k.sixteen);
+            const bf16x8 q = codes8(c[r][S], k.fields, k.sixteen);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[n], q, begins ? zero : acc[r][n], 0, 0, 0);
@@ -375,11 +292,11 @@ __device__ __forceinline__ void multiply_unit(const Unit<RL, NT, RT, MG>& v, con
         if constexpr (ends) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const uint32_t w = v.m[r][S / (4 / MG)];
+                const uint32_t w = m[r][S / (4 / MG)];
                 const float z = __uint_as_float(w & 0xFFFF0000u);
-                // the scale of either type by a bit select: no branch between the loads
+                // the scale of either type by a bit select, without a branch
                 const uint32_t half = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)w));
-                const float s = __uint_as_float(((half & k.f16) | ((w << 16) & ~k.f16)) & live);
+                const float s = __uint_as_float((half & k.f16) | ((w << 16) & ~k.f16));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -425,168 +342,191 @@ __device__ __forceinline__ void store_totals(float* red, const floatx4 (&tot)[RT
 __device__ __forceinline__ int total_row(int v) { return (v >> 8) * 16 + ((v & 63) >> 4) * 4 + ((v >> 6) & 3); }
 __device__ __forceinline__ int total_col(int v) { return v & 15; }
 
-// Plain and SwiGLU. A work item is a pass and RT tiles of 16 rows. A workgroup
-// takes a contiguous share of the items; of these every wave takes whole ones, one
-// after another, and stores them itself, as long as there are W more. The units
-// of the rest are one line, cut into W pieces: a piece is part of two items at
-// most, and what the waves summed of an item is added through LDS, in wave order.
-// So all waves stream all the time, and meet once. Units go by Q in a turn (the
-// last ones past the row count for nothing): as the products of one are done,
-// the same one of the next turn is loaded.
-template <bool SWIGLU, int RL, int NT, int RT, int MG, int W, int Q>
-__global__ __launch_bounds__(W * kWave) void int4_kernel(Int4Args a)
-{
-    static_assert(NT == 1 || RL == 16, "rows");
-    constexpr int CP = RL * NT, NV = RT * NT * 256;
-    __shared__ Passes ps;
-    __shared__ int first_item[W];
-    __shared__ float red[W][2][NV];
-
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int units = units_of(a.K), turns = (units + Q - 1) / Q, tiles = tiles_of(a.N, SWIGLU), groups = tiles / RT;
-    const uint32_t items = (uint32_t)(build_passes<CP, W>(ps, a) * groups);
-    const int M = SWIGLU ? a.N / 2 : a.N;
-    const Consts consts(a);
-    const __amdgpu_buffer_rsrc_t xb = x_buffer(a);
-
-    const uint32_t share = items / gridDim.x, more = items % gridDim.x;
-    const int mine = (int)(share + (blockIdx.x < more ? 1 : 0));
-    const int i0 = (int)(blockIdx.x * share + min(blockIdx.x, more));
-    const int full = mine / W, rest = mine % W, rest0 = i0 + full * W;
-    const uint32_t line = (uint32_t)(rest * turns);
-    const int cut0 = (int)(line * wv / W), cut1 = (int)(line * (wv + 1) / W);  // this wave's piece
-    const int first = (int)((uint32_t)cut0 / (uint32_t)turns);               // its first item of the rest
-    const int segments = full + (cut1 > cut0) + (cut1 > (first + 1) * turns);
-    if (lane == 0)
-        first_item[wv] = first;
-    struct Segment {
-        int item, q0, q1;
-    };
-    auto segment = [&](int k) {
-        if (k < full)
-            return Segment{i0 + k * W + wv, 0, turns};
-        const int m = first + k - full;
-        return Segment{rest0 + m, max(cut0 - m * turns, 0), min(cut1 - m * turns, turns)};
+// A wave's way through units of weights and the x rows that go with them: Q units
+// are in flight, and a unit's registers are loaded again before it is multiplied.
+//
+// In the order of the products' operands, 64 lanes of a load of x would read 16
+// rows in pieces of 16 bytes, at four times the cache's time for whole lines, and
+// that was most of the work from 8 rows on. So a load takes 256 bytes (a unit's k)
+// of each of four rows, L loads for the 4 L rows of a pass (NT times 16 with L = 4),
+// and the wave turns them in its own 4 KiB of LDS per 16 rows: piece p of row r is at
+// place p ^ r of its row, so that neither side has bank conflicts. Rows of the 16
+// that were not loaded hold anything: a row of the products depends on its own
+// row of x. (4096 x 4096, 12 rows: 7.9 -> 5.0 us, 64: 20.2 -> 8.3; 14336 x 4096, 128 rows:
+// 69.5 -> 29.4.)
+template <int L, int NT, int RT, int MG, int Q>
+struct Stream {
+    static_assert(NT == 1 || L == 4, "rows");
+    typedef uint32_t Meta __attribute__((ext_vector_type(MG)));
+    typedef const __attribute__((address_space(1))) Vec16* Codes;
+    typedef const __attribute__((address_space(1))) Meta* Metas;
+    struct Slot {
+        Vec16 c[RT], x[NT][L];
+        Meta m[RT];
     };
 
-    // The load cursor. Past the last segment it stays where it is.
-    Cursor<NT> at;
-    int lk = 0, lend = 0;
-    auto aim_at = [&]() {
-        const Segment s = segment(lk);
-        const int pass = (int)((uint32_t)s.item / (uint32_t)groups), tg = s.item - pass * groups;
-        const Pass p = ps.pass[pass];
+    const Int4Args& a;
+    const Passes& ps;
+    const Consts& consts;
+    __amdgpu_buffer_rsrc_t xb;
+    int units, lane;
+    Vec16* turn;         // [NT][16 rows][16 pieces]
+    int to[L], from[4];  // places of load i's piece, of step i's
+    uint32_t xo[NT][L];  // offsets of the rows of x
+    Global c, m;         // the next unit's codes and groups
+    int u;               // and its number
+
+    __device__ __forceinline__ Stream(const Int4Args& args, const Passes& passes, const Consts& k, Vec16* place)
+        : a(args), ps(passes), consts(k), xb(x_buffer(args)), units(units_of(args.K)), lane(threadIdx.x % kWave),
+          turn(place)
+    {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = n * 16 + (lane % RL);
-            at.xo[n] = row >= p.count ? kNoRow : ps.row[p.start + row].x + (lane >> 4) * 16;
+        for (int i = 0; i < L; ++i) {
+            const int row = 4 * i + (lane >> 4);
+            to[i] = row * 16 + ((lane & 15) ^ row);
         }
-        aim<NT, MG>(at, a, (int64_t)__builtin_amdgcn_readfirstlane((int)p.expert) * tiles + tg * RT, units, s.q0 * Q);
-        lend = s.q1 * Q;
-    };
-    auto advance = [&]() {
-        if (at.u + Q < lend) {
-            at.u += Q;
-            at.c += Q * 1024;
-            at.m += Q * 64 * MG;
-        } else if (lk + 1 < segments) {
-            ++lk;
-            aim_at();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            from[i] = (lane & 15) * 16 + ((4 * i + (lane >> 4)) ^ (lane & 15));
+    }
+    // Next: unit `unit` of pass p and tiles t.. of its expert's `tiles`.
+    __device__ __forceinline__ void aim(const Pass& p, int tiles, int t, int unit)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int row = n * 16 + 4 * i + (lane >> 4);
+                xo[n][i] = row >= p.count ? kNoRow : ps.row[p.start + row].x + (lane & 3) * 16;
+            }
+        const int64_t tile = (int64_t)__builtin_amdgcn_readfirstlane((int)p.expert) * tiles + t;
+        c = uniform((const uint8_t*)a.codes + (tile * units + unit) * 1024);
+        m = uniform((const uint8_t*)a.meta + (tile * units + unit) * (64 * MG));
+        u = unit;
+    }
+    __device__ __forceinline__ void load(Slot& v)
+    {
+        const uint32_t co = lane * 16, mo = (lane & 15) * 4 * MG;
+        // behind the row (K % 128): its end again, times a scale of 0
+        const int k = min(u * kUnitK + 32 * ((lane & 15) >> 2), a.K - 32) * 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                v.x[n][i] = __builtin_bit_cast(Vec16, __builtin_amdgcn_raw_buffer_load_b128(xb, (int)xo[n][i] + k, 0, 0));
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            v.c[r] = __builtin_nontemporal_load((Codes)(c + (int64_t)r * units * 1024 + co));
+            v.m[r] = *(Metas)(m + (int64_t)r * units * (64 * MG) + mo);
         }
-    };
-    // Row `row` of a pass, weight rows col of the item's RT tiles: sums v[r].
-    auto store = [&](int pass, int tg, int row, int col, const float (&v)[RT]) {
-        const Pass p = ps.pass[pass];
-        if (row >= p.count)
-            return;
-        const int64_t y = (int64_t)ps.row[p.start + row].assigned * M;
-        if constexpr (SWIGLU) {
-            const int n = tg * 16 + col;
-            if (n < M)
-                store_y(a, y + n, silu_f32(v[0]) * v[1]);
-        } else {
+        c += 1024;
+        m += 64 * MG;
+        ++u;
+        __builtin_amdgcn_sched_barrier(0);  // here and in this order, not behind the products that follow
+    }
+    // n units from where it aims: next() before each but the first is loaded,
+    // done(tot, last) after each is multiplied.
+    template <class Next, class Done>
+    __device__ __forceinline__ void run(int n, floatx4 (&tot)[RT][NT], Next next, Done done)
+    {
+        Slot v[Q];
+#pragma unroll
+        for (int j = 0; j < Q; ++j)
+            if (j < n) {
+                if (j > 0)
+                    next();
+                load(v[j]);
+            }
+        auto step = [&](Slot& slot, bool more, bool last) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < L; ++i)
+                    turn[t * 256 + to[i]] = slot.x[t][i];
+            Vec16 codes[RT];
+            Meta groups[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int n = (tg * RT + r) * 16 + col;
-                if (n < M)
-                    store_y(a, y + n, v[r]);
+                codes[r] = slot.c[r];
+                groups[r] = slot.m[r];
             }
-        }
-    };
-
-    if (segments > 0) {
-        aim_at();
-        Unit<RL, NT, RT, MG> v[Q];
+            if (more) {
+                next();
+                load(slot);
+            }
+            multiply_unit<NT, RT, MG>([&](auto s, int t) { return as_bf16x8(turn[t * 256 + from[s()]]); }, codes, groups,
+                                      consts, tot);
+            done(tot, last);
+        };
+        int i = 0;
+        for (; i + 2 * Q <= n; i += Q) {
 #pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            load_unit(v[j], a, xb, at, units, j);
-            __builtin_amdgcn_sched_barrier(0);  // in this order, for the waits in the loop
+            for (int j = 0; j < Q; ++j)
+                step(v[j], true, false);
         }
+#pragma unroll
+        for (int j = 0; j < Q; ++j)
+            if (i + j < n)
+                step(v[j], i + j + Q < n, i + j + 1 == n);
+#pragma unroll
+        for (int j = 0; j < Q - 1; ++j)
+            if (i + Q + j < n)
+                step(v[j], false, i + Q + j + 1 == n);
+    }
+};
+
+// Plain and SwiGLU. A work item is a pass and RT tiles; the waves cut its units
+// into W pieces and add their sums in wave order.
+template <bool SWIGLU, int L, int NT, int RT, int MG, int W, int Q>
+__global__ __launch_bounds__(W * kWave, 2) void int4_kernel(Int4Args a)
+{
+    static_assert(RT <= 4, "a wave's sums fit where x was");
+    __shared__ Passes ps;
+    __shared__ Vec16 turn[W][NT * 256];
+
+    const int tid = threadIdx.x;
+    const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int units = units_of(a.K), tiles = tiles_of(a.N, SWIGLU), groups = (tiles + RT - 1) / RT;
+    const int items = build_passes<4 * L * NT, W>(ps, a) * groups;
+    const int M = SWIGLU ? a.N / 2 : a.N;
+    const int u0 = units * wv / W, u1 = units * (wv + 1) / W;
+    const Consts consts(a);
+    Stream<L, NT, RT, MG, Q> stream(a, ps, consts, turn[wv]);
+
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int pass = (int)((uint32_t)item / (uint32_t)groups);
+        // the last tiles: a few of the group before again, with the same results
+        const int t = min((item - pass * groups) * RT, tiles - RT);
+        const Pass p = ps.pass[pass];
         floatx4 tot[RT][NT];
         clear(tot);
-        int k = 0;
-        Segment now = segment(0);
-        for (;;) {
-            advance();
-#pragma unroll
-            for (int j = 0; j < Q; ++j) {
-                multiply_unit(v[j], consts, tot, j == 0 || now.q0 * Q + j < units ? ~0u : 0u);
-                load_unit(v[j], a, xb, at, units, j);
-            }
-            if (++now.q0 < now.q1)
-                continue;
-            if (k < full) {
-                const int pass = (int)((uint32_t)now.item / (uint32_t)groups), tg = now.item - pass * groups;
-#pragma unroll 1
-                for (int t = 0; t < NT; ++t)
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        float w[RT];
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-                            w[r] = NT == 1 ? tot[r][0][i] : tot[r][t][i];
-                        store(pass, tg, t * 16 + (lane >> 4) * 4 + i, lane & 15, w);
-                    }
-            } else {
-                store_totals(red[wv][k - full], tot);
-            }
-            clear(tot);
-            if (++k == segments)
-                break;
-            now = segment(k);
+        if (u0 < u1) {
+            stream.aim(p, tiles, t, u0);
+            stream.run(u1 - u0, tot, [] {}, [](auto&, bool) {});
         }
-    }
-    if (rest > 0) {
+        store_totals((float*)turn[wv], tot);
         lds_barrier();
-        const int firsts = first_item[lane % W];
-        for (int i = tid; i < rest * NT * 256; i += W * kWave) {
-            const int m = __builtin_amdgcn_readfirstlane(i / (NT * 256)), v = i % (NT * 256);
+        for (int v = tid; v < NT * 256; v += W * kWave) {
             float sum[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
                 sum[r] = 0.0f;
-#pragma unroll 1
-            for (int w0 = 0; w0 < W; w0 += 4) {  // the waves with a piece of item m, in order
-                float p[4][RT];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int w = w0 + j, c0 = (int)(line * w / W), c1 = (int)(line * (w + 1) / W);
-                    const bool has = c0 < c1 && c0 < (m + 1) * turns && c1 > m * turns;
-                    const float* t = &red[w][has ? m - __builtin_amdgcn_readlane(firsts, w) : 0][v];
+            for (int w = 0; w < W; ++w)
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        p[j][r] = has ? t[r * NT * 256] : 0.0f;
+                for (int r = 0; r < RT; ++r)
+                    sum[r] += ((const float*)turn[w])[r * NT * 256 + v];
+            if (total_row(v) < p.count) {
+                const int64_t y = (int64_t)ps.row[p.start + total_row(v)].assigned * M;
+#pragma unroll
+                for (int r = 0; r < RT; r += SWIGLU ? 2 : 1) {
+                    const int n = (SWIGLU ? (t + r) / 2 : t + r) * 16 + total_col(v);
+                    if (n < M)
+                        store_y(a, y + n, SWIGLU ? silu_f32(sum[r]) * sum[r + SWIGLU] : sum[r]);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        sum[r] += p[j][r];
             }
-            const int pass = (int)((uint32_t)(rest0 + m) / (uint32_t)groups);
-            store(pass, rest0 + m - pass * groups, total_row(v), total_col(v), sum);
         }
+        lds_barrier();
     }
     if (ps.none)  // assignments of no expert: rows of zeros
         for (int p = 0; p < a.T * a.k; ++p)
@@ -599,67 +539,40 @@ __global__ __launch_bounds__(W * kWave) void int4_kernel(Int4Args a)
 // the units of all passes are one line, cut into W pieces, one per wave. At the
 // end of a pass, or of its piece, a wave adds w times what it summed to its own
 // sums of the tokens in LDS, and these are added once, in wave order.
-template <int RL, int RT, int MG, int W, int Q>
+template <int L, int RT, int MG, int W>
 __global__ __launch_bounds__(W * kWave) void int4_sum_kernel(Int4Args a)
 {
-    __shared__ Passes ps;
-    extern __shared__ float sums[];  // [W][T][16 RT]
     constexpr int C = 16 * RT;
+    __shared__ Passes ps;
+    __shared__ Vec16 turn[W][256];
+    extern __shared__ float sums[];  // [W][T][C]
 
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wv = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int units = units_of(a.K), turns = (units + Q - 1) / Q, tiles = tiles_of(a.N, 0);
-    const int tg = blockIdx.x;
+    const int units = units_of(a.K), tiles = tiles_of(a.N, 0), t = blockIdx.x * RT;
     for (int i = tid; i < W * a.T * C; i += W * kWave)
         sums[i] = 0.0f;
-    const uint32_t line = (uint32_t)(build_passes<RL, W>(ps, a) * turns);
+    const uint32_t line = (uint32_t)(build_passes<4 * L, W>(ps, a) * units);
     const int cut0 = (int)(line * wv / W), cut1 = (int)(line * (wv + 1) / W);
     const Consts consts(a);
-    const __amdgpu_buffer_rsrc_t xb = x_buffer(a);
+    Stream<L, 1, RT, MG, 2> stream(a, ps, consts, turn[wv]);
 
     if (cut1 > cut0) {
-        // The load cursor: `left` turns to the end of the piece, where it stays.
-        Cursor<1> at;
-        int lp = (int)((uint32_t)cut0 / (uint32_t)turns), left = cut1 - cut0;
-        auto aim_at = [&](int q) {
-            const Pass p = ps.pass[lp];
-            at.xo[0] = lane % RL >= p.count ? kNoRow : ps.row[p.start + lane % RL].x + (lane >> 4) * 16;
-            aim<1, MG>(at, a, (int64_t)__builtin_amdgcn_readfirstlane((int)p.expert) * tiles + tg * RT, units, q * Q);
+        int loading = (int)((uint32_t)cut0 / (uint32_t)units);  // the pass whose units are loaded next
+        int pass = loading, to_end = units - (cut0 - pass * units);
+        stream.aim(ps.pass[pass], tiles, t, cut0 - pass * units);
+        floatx4 tot[RT][1];
+        clear(tot);
+        auto next = [&] {
+            if (stream.u == units)
+                stream.aim(ps.pass[++loading], tiles, t, 0);
         };
-        auto advance = [&]() {
-            if (--left <= 0)
+        auto done = [&](floatx4(&tot)[RT][1], bool last) {
+            if (--to_end > 0 && !last)
                 return;
-            if (at.u + Q < units) {
-                at.u += Q;
-                at.c += Q * 1024;
-                at.m += Q * 64 * MG;
-            } else {
-                ++lp;
-                aim_at(0);
-            }
-        };
-        int p = lp, q = cut0 - p * turns, todo = cut1 - cut0;
-        aim_at(q);
-        Unit<RL, 1, RT, MG> v[Q];
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            load_unit(v[j], a, xb, at, units, j);
-            __builtin_amdgcn_sched_barrier(0);  // in this order, for the waits in the loop
-        }
-        floatx4 sum[RT][1];
-        clear(sum);
-        for (;;) {
-            advance();
-#pragma unroll
-            for (int j = 0; j < Q; ++j) {
-                multiply_unit(v[j], consts, sum, j == 0 || q * Q + j < units ? ~0u : 0u);
-                load_unit(v[j], a, xb, at, units, j);
-            }
-            if (++q < turns && --todo > 0)
-                continue;
             // a token has one row in a pass, unless it has the expert twice: then
             // the lane groups take turns
-            const Pass now = ps.pass[p];
+            const Pass now = ps.pass[pass++];
             const int groups = ps.twins ? 4 : 1;
 #pragma unroll 1
             for (int g = 0; g < groups; ++g)
@@ -671,23 +584,17 @@ __global__ __launch_bounds__(W * kWave) void int4_sum_kernel(Int4Args a)
                         float* y = sums + (wv * a.T + o.token) * C + (lane & 15);
 #pragma unroll
                         for (int r = 0; r < RT; ++r)
-                            y[r * 16] = fmaf(o.w, sum[r][0][i], y[r * 16]);
+                            y[r * 16] = fmaf(o.w, tot[r][0][i], y[r * 16]);
                     }
                 }
-            clear(sum);
-            if (q == turns) {
-                q = 0;
-                ++p;
-                if (--todo <= 0)
-                    break;
-            } else {
-                break;
-            }
-        }
+            clear(tot);
+            to_end = units;
+        };
+        stream.run(cut1 - cut0, tot, next, done);
     }
     lds_barrier();
     for (int v = tid; v < a.T * C; v += W * kWave) {
-        const int n = tg * C + v % C;
+        const int n = t * 16 + v % C;
         float s = sums[v];
 #pragma unroll
         for (int w = 1; w < W; ++w)
@@ -714,69 +621,72 @@ hipError_t by_groups(int group, Go go)
     return hipGetLastError();
 }
 
-template <bool SWIGLU, int RL, int NT, int RT, int W, int Q = 2>
+template <bool SWIGLU, int L, int NT, int RT, int W, int Q>
 hipError_t launch(const Int4Args& a, int per_cu, int cus, hipStream_t s)
 {
-    const int groups = tiles_of(a.N, SWIGLU) / RT, A = a.T * a.k, CP = RL * NT;
+    const int groups = (tiles_of(a.N, SWIGLU) + RT - 1) / RT, A = a.T * a.k, CP = 4 * L * NT;
     // at most: every expert's passes
     const int64_t passes = a.ids ? std::min(a.E, A) + A / CP : (A + CP - 1) / CP;
     const unsigned grid = (unsigned)std::min<int64_t>(passes * groups, (int64_t)cus * per_cu);
     return by_groups(a.group, [&](auto mg) {
-        hipLaunchKernelGGL((int4_kernel<SWIGLU, RL, NT, RT, decltype(mg)::value, W, Q>), dim3(grid), dim3(W * kWave), 0, s, a);
+        hipLaunchKernelGGL((int4_kernel<SWIGLU, L, NT, RT, decltype(mg)::value, W, Q>), dim3(grid), dim3(W * kWave), 0, s,
+                           a);
     });
 }
 
-template <int RL, int RT, int Q>
+template <int L, int RT, int W>
 hipError_t launch_sum(const Int4Args& a, hipStream_t s)
 {
-    constexpr int W = 16;
     const unsigned grid = (unsigned)(tiles_of(a.N, 0) / RT);
     const size_t lds = (size_t)W * a.T * 16 * RT * sizeof(float);
     return by_groups(a.group, [&](auto mg) {
-        hipLaunchKernelGGL((int4_sum_kernel<RL, RT, decltype(mg)::value, W, Q>), dim3(grid), dim3(W * kWave), lds, s, a);
+        hipLaunchKernelGGL((int4_sum_kernel<L, RT, decltype(mg)::value, W>), dim3(grid), dim3(W * kWave), lds, s, a);
     });
 }
 
 // Two tiles per workgroup where that leaves one for every compute unit and the
-// sums of the tokens fit (N = 8192: 36.7 -> 27.7 us; with too few, N = 4096, 53 ->
-// 67). Four units in a turn for long rows (K = 14336: 53 -> 49 us; K = 2048: 8.6 ->
-// 9.8).
-template <int RL>
+// sums of the tokens fit (4 tokens on 8 experts of 14336 x 4096: 32.0 us, one tile
+// 38.6). Else sixteen waves, for the units in flight (16 tokens on 128 experts
+// of 2048 x 768: 19.3 us, eight waves 24.3), but for the loads of many rows (64 tokens
+// on 8 experts of 4096 x 1408: 15.6, sixteen 16.1) and sums that don't fit so.
+template <int L>
 hipError_t launch_sums(const Int4Args& a, int cus, hipStream_t s)
 {
     if (tiles_of(a.N, 0) / 2 >= cus && a.T <= 64)
-        return launch_sum<RL, 2, 2>(a, s);
-    if constexpr (RL < 16) {
-        if (a.K >= 8192)
-            return launch_sum<RL, 1, 4>(a, s);
+        return launch_sum<L, 2, 8>(a, s);
+    if constexpr (L < 4) {
+        if (a.T <= 64)
+            return launch_sum<L, 1, 16>(a, s);
     }
-    return launch_sum<RL, 1, 2>(a, s);
+    return launch_sum<L, 1, 8>(a, s);
 }
 
-// Many items: four workgroups of four waves per compute unit, whose starts and
-// ends overlap the others' streaming (16 tokens over 128 experts of 1536 x 2048:
-// 23.3 us, two of eight waves 24.7, one of sixteen 28; 8 experts of 28672 x 4096, one
-// token: 26.5, 29.6, 31.6). Few: eight waves for an item (one token, 4096 x 4096: 5.8
-// us, 6.5 with four; K = 14336: 10.8, 14.2).
-template <int RL, int NT>
+// The more items, the more tiles each, so that x is read less often, and the fewer
+// waves, so that starts and ends of workgroups overlap the others' streaming.
+// One token, K = 4096: N = 4096 (256 tiles) 4.8 us with one tile and eight waves, 5.8
+// with two; 14336: 8.4 with two tiles and four waves, 9.2 and 9.5 with one and
+// four; 28672: 13.1 with four, 13.5 with two. Of long rows each wave has enough:
+// four tiles and eight waves (12 rows, 14336 x 14336: 24.1 us, two and four 29.5).
+template <int L, int NT>
 hipError_t launch_items(const Int4Args& a, int cus, hipStream_t s)
 {
-    const int A = a.T * a.k, CP = RL * NT;
+    const int A = a.T * a.k, CP = 4 * L * NT;
     const int64_t passes = a.ids ? std::min(a.E, A) : (A + CP - 1) / CP;
     const int64_t tiles = passes * tiles_of(a.N, a.swiglu);
+    if (!a.swiglu && tiles <= cus)
+        return launch<false, L, NT, 1, 8, NT == 1 ? 2 : 1>(a, 2, cus, s);
+    if (tiles <= 2 * cus)
+        return a.swiglu ? launch<true, L, NT, 2, 8, 1>(a, 2, cus, s) : launch<false, L, NT, 2, 8, 1>(a, 2, cus, s);
+    // a group of four tiles needs four (passes are 128 at most)
     if constexpr (NT == 1) {
-        if (a.swiglu)
-            return tiles / 2 >= 2 * cus ? launch<true, RL, 1, 2, 4>(a, 4, cus, s) : launch<true, RL, 1, 2, 8>(a, 2, cus, s);
-        if (tiles / 2 >= 2 * cus)
-            return launch<false, RL, 1, 2, 4>(a, 4, cus, s);
-        return tiles >= 2 * cus ? launch<false, RL, 1, 1, 4>(a, 4, cus, s) : launch<false, RL, 1, 1, 8>(a, 2, cus, s);
-    } else {
-        if (a.swiglu)
-            return launch<true, 16, NT, 2, 4, 1>(a, 2, cus, s);
-        if (tiles / 2 >= 2 * cus)
-            return launch<false, 16, NT, 2, 4, 1>(a, 2, cus, s);
-        return launch<false, 16, NT, 1, 4, 1>(a, 3, cus, s);
+        if (a.K >= 8192 && tiles_of(a.N, a.swiglu) >= 4)
+            return a.swiglu ? launch<true, L, 1, 4, 8, 1>(a, 1, cus, s) : launch<false, L, 1, 4, 8, 1>(a, 1, cus, s);
+        if (tiles <= 6 * cus || tiles_of(a.N, a.swiglu) < 4)
+            return a.swiglu ? launch<true, L, 1, 2, 4, 1>(a, 4, cus, s) : launch<false, L, 1, 2, 4, 1>(a, 4, cus, s);
+    } else if (tiles_of(a.N, a.swiglu) < 4) {
+        return a.swiglu ? launch<true, L, NT, 2, 8, 1>(a, 2, cus, s) : launch<false, L, NT, 2, 8, 1>(a, 2, cus, s);
     }
+    return a.swiglu ? launch<true, L, NT, 4, 4, 1>(a, 2, cus, s) : launch<false, L, NT, 4, 4, 1>(a, 2, cus, s);
 }
 
 }  // namespace
@@ -802,22 +712,22 @@ hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s)
 {
     const int A = a.T * a.k;
     // The rows that passes hold: with ids, the mean of the chosen experts' (if all
-    // choose alike), in eighths. Fewer rows per pass make loads of x cheaper, but
-    // an expert of more is read again: passes of 4 up to 1.6 rows, of 8 up to 4.5 (16
-    // tokens on 8 experts, 4 rows each: 8 rows 91.6 us, 4 rows 122, 16 rows 91.8).
+    // choose alike), in eighths. Fewer rows per pass need fewer loads of x, but
+    // an expert of more is read again: passes of 4 up to 1.6 rows, of 8 up to 4.5, of
+    // 16 up to 12, else of 32 (64 tokens on 8 experts of 8192 x 4096, 16 rows each: 38.7 us,
+    // passes of 16 40.7). A weighted sum stays at 16, whose tokens' sums take the LDS.
     const int rows = !a.ids ? a.T * 8 : a.T <= 4 ? 8 : std::min(a.T * 8, A * 8 / std::min(a.E, A));
+    const int few = a.ids ? 13 : 32, some = a.ids ? 36 : 64, more = a.ids ? 96 : 128;
     if (a.w) {
-        if (rows <= 13)
-            return launch_sums<4>(a, cus, s);
-        return rows <= 36 ? launch_sums<8>(a, cus, s) : launch_sums<16>(a, cus, s);
+        if (rows <= few)
+            return launch_sums<1>(a, cus, s);
+        return rows <= some ? launch_sums<2>(a, cus, s) : launch_sums<4>(a, cus, s);
     }
-    if (rows <= (a.ids ? 13 : 32))
-        return launch_items<4, 1>(a, cus, s);
-    if (rows <= (a.ids ? 36 : 64))
-        return launch_items<8, 1>(a, cus, s);
-    if (rows <= 128)
-        return launch_items<16, 1>(a, cus, s);
-    return rows <= 256 ? launch_items<16, 2>(a, cus, s) : launch_items<16, 4>(a, cus, s);
+    if (rows <= few)
+        return launch_items<1, 1>(a, cus, s);
+    if (rows <= some)
+        return launch_items<2, 1>(a, cus, s);
+    return rows <= more ? launch_items<4, 1>(a, cus, s) : launch_items<4, 2>(a, cus, s);
 }
 
 }  // namespace cmoe
