@@ -661,32 +661,33 @@ hipError_t launch_sums(const Int4Args& a, int cus, hipStream_t s)
     return launch_sum<L, 1, 8>(a, s);
 }
 
+// Tiles times the passes of `rows` rows: with ids, if all experts are chosen alike.
+int64_t tile_passes(const Int4Args& a, int rows)
+{
+    const int A = a.T * a.k;
+    return (int64_t)(a.ids ? std::min(a.E, A) : (A + rows - 1) / rows) * tiles_of(a.N, a.swiglu);
+}
+
 // The more items, the more tiles each, so that x is read less often, and the fewer
 // waves, so that starts and ends of workgroups overlap the others' streaming.
 // One token, K = 4096: N = 4096 (256 tiles) 4.8 us with one tile and eight waves, 5.8
 // with two; 14336: 8.4 with two tiles and four waves, 9.2 and 9.5 with one and
 // four; 28672: 13.1 with four, 13.5 with two. Of long rows each wave has enough:
 // four tiles and eight waves (12 rows, 14336 x 14336: 24.1 us, two and four 29.5).
-template <int L, int NT>
+template <int L>
 hipError_t launch_items(const Int4Args& a, int cus, hipStream_t s)
 {
-    const int A = a.T * a.k, CP = 4 * L * NT;
-    const int64_t passes = a.ids ? std::min(a.E, A) : (A + CP - 1) / CP;
-    const int64_t tiles = passes * tiles_of(a.N, a.swiglu);
+    const int64_t tiles = tile_passes(a, 4 * L);
+    const bool four = tiles_of(a.N, a.swiglu) >= 4;
     if (!a.swiglu && tiles <= cus)
-        return launch<false, L, NT, 1, 8, NT == 1 ? 2 : 1>(a, 2, cus, s);
+        return launch<false, L, 1, 1, 8, 2>(a, 2, cus, s);
     if (tiles <= 2 * cus)
-        return a.swiglu ? launch<true, L, NT, 2, 8, 1>(a, 2, cus, s) : launch<false, L, NT, 2, 8, 1>(a, 2, cus, s);
-    // a group of four tiles needs four (passes are 128 at most)
-    if constexpr (NT == 1) {
-        if (a.K >= 8192 && tiles_of(a.N, a.swiglu) >= 4)
-            return a.swiglu ? launch<true, L, 1, 4, 8, 1>(a, 1, cus, s) : launch<false, L, 1, 4, 8, 1>(a, 1, cus, s);
-        if (tiles <= 6 * cus || tiles_of(a.N, a.swiglu) < 4)
-            return a.swiglu ? launch<true, L, 1, 2, 4, 1>(a, 4, cus, s) : launch<false, L, 1, 2, 4, 1>(a, 4, cus, s);
-    } else if (tiles_of(a.N, a.swiglu) < 4) {
-        return a.swiglu ? launch<true, L, NT, 2, 8, 1>(a, 2, cus, s) : launch<false, L, NT, 2, 8, 1>(a, 2, cus, s);
-    }
-    return a.swiglu ? launch<true, L, NT, 4, 4, 1>(a, 2, cus, s) : launch<false, L, NT, 4, 4, 1>(a, 2, cus, s);
+        return a.swiglu ? launch<true, L, 1, 2, 8, 1>(a, 2, cus, s) : launch<false, L, 1, 2, 8, 1>(a, 2, cus, s);
+    if (four && a.K >= 8192)
+        return a.swiglu ? launch<true, L, 1, 4, 8, 1>(a, 1, cus, s) : launch<false, L, 1, 4, 8, 1>(a, 1, cus, s);
+    if (four && tiles > 6 * cus)
+        return a.swiglu ? launch<true, L, 1, 4, 4, 1>(a, 2, cus, s) : launch<false, L, 1, 4, 4, 1>(a, 2, cus, s);
+    return a.swiglu ? launch<true, L, 1, 2, 4, 1>(a, 4, cus, s) : launch<false, L, 1, 2, 4, 1>(a, 4, cus, s);
 }
 
 }  // namespace
@@ -714,8 +715,7 @@ hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s)
     // The rows that passes hold: with ids, the mean of the chosen experts' (if all
     // choose alike), in eighths. Fewer rows per pass need fewer loads of x, but
     // an expert of more is read again: passes of 4 up to 1.6 rows, of 8 up to 4.5, of
-    // 16 up to 12, else of 32 (64 tokens on 8 experts of 8192 x 4096, 16 rows each: 38.7 us,
-    // passes of 16 40.7). A weighted sum stays at 16, whose tokens' sums take the LDS.
+    // 16 up to 12. A weighted sum stays at 16, whose tokens' sums take the LDS.
     const int rows = !a.ids ? a.T * 8 : a.T <= 4 ? 8 : std::min(a.T * 8, A * 8 / std::min(a.E, A));
     const int few = a.ids ? 13 : 32, some = a.ids ? 36 : 64, more = a.ids ? 96 : 128;
     if (a.w) {
@@ -724,10 +724,15 @@ hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s)
         return rows <= some ? launch_sums<2>(a, cus, s) : launch_sums<4>(a, cus, s);
     }
     if (rows <= few)
-        return launch_items<1, 1>(a, cus, s);
+        return launch_items<1>(a, cus, s);
     if (rows <= some)
-        return launch_items<2, 1>(a, cus, s);
-    return rows <= more ? launch_items<4, 1>(a, cus, s) : launch_items<4, 2>(a, cus, s);
+        return launch_items<2>(a, cus, s);
+    // Passes of 32 rows spend less on each unit, but only where there are enough
+    // of them for the card (64 rows, K = 4096: N = 8192 12.5 us, passes of 16 13.1; N = 2048
+    // 6.7 and 6.1; 128 rows of 14336 x 4096 35.5 and 43.0).
+    if (rows <= more || tile_passes(a, 16) <= 4 * cus || tiles_of(a.N, a.swiglu) < 4)
+        return launch_items<4>(a, cus, s);
+    return a.swiglu ? launch<true, 4, 2, 4, 4, 1>(a, 2, cus, s) : launch<false, 4, 2, 4, 4, 1>(a, 2, cus, s);
 }
 
 }  // namespace cmoe
