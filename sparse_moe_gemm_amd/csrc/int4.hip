@@ -210,11 +210,11 @@ __device__ __forceinline__ int build_passes(Passes& p, const Int4Args& a)
 }
 
 // SiLU to a few fp32 steps over the whole range (outputs may be fp32): the
-// exponential never overflows.
+// exponential never overflows, and a sum that did, to -infinity, gives -0.
 __device__ __forceinline__ float silu_f32(float z)
 {
     const float e = expf(-fabsf(z));
-    return (z < 0.0f ? z * e : z) / (1.0f + e);
+    return (z < 0.0f ? fmaxf(z, -0x1.fffffep127f) * e : z) / (1.0f + e);
 }
 
 __device__ __forceinline__ void store_y(const Int4Args& a, int64_t at, float v)

@@ -318,6 +318,14 @@ def test_int4_linear_refusals(kw, status):
     assert cm.colibri_moe_int4_linear(None, FAKE, FAKE, 4, 2, 0, FAKE, None, FAKE, cm.BF16) == cm.ERR_INVALID_ARG
 
 
+def test_int4_linear_refuses_y_over_x():
+    """x [4][256] bf16 takes 2048 bytes, y [4][2][64] bf16 1024, fp32 2048."""
+    for y in (FAKE, FAKE + 2032, FAKE - 1008):
+        assert c_linear(x=FAKE, y=y) == cm.ERR_INVALID_ARG
+    assert c_linear(x=FAKE, y=FAKE - 2032, dtype=cm.F32) == cm.ERR_INVALID_ARG
+    assert c_linear(x=FAKE, y=FAKE + 4080, per_slot=1) == cm.ERR_INVALID_ARG
+
+
 def test_int4_codec_arguments(dev, monkeypatch):
     calls = []
     for fn in ("colibri_moe_quantize_int4", "colibri_moe_dequantize_int4"):

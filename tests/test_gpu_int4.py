@@ -93,6 +93,32 @@ def test_codec_special_groups():
     assert abs(back[0, 5].item() - 3e38) <= 4e37 and abs(back[0, 9].item() + 3e38) <= 4e37 and back[0, 0].item() == 0
 
 
+@pytest.mark.parametrize("symmetric", [False, True])
+def test_codes_are_those_of_fp32_division(symmetric):
+    """Values on the ties between codes and one float beside them, under scales of
+    every exponent: rint of the IEEE quotient w / s, plus z."""
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    rng = np.random.default_rng(7)
+    rows, group = 4096, 32
+    s = ((1 + rng.integers(0, 128, rows) / 128) * 2.0 ** rng.integers(-124, 122, rows)).astype(np.float32)
+    z = np.full(rows, 8) if symmetric else rng.integers(0, 16, rows)
+    w = ((rng.integers(-z[:, None], 15 - z[:, None], (rows, group)) + 0.5) * s[:, None].astype(np.float64)).astype(np.float32)
+    side = rng.integers(-1, 2, w.shape)
+    w = np.where(side < 0, np.nextafter(w, np.float32(-np.inf)), np.where(side > 0, np.nextafter(w, np.float32(np.inf)), w))
+    lo, hi = ((-7, 7) if symmetric else (-z, 15 - z))
+    w = np.clip(w, (lo * s)[:, None], (hi * s)[:, None]).astype(np.float32)
+    w[:, 0], w[:, 1] = lo * s, hi * s  # the group's scale is s, its zero point z
+    codes, scales, zeros = cm.quantize_int4(torch.from_numpy(w).cuda(), group, symmetric=symmetric)
+    torch.cuda.synchronize()
+    assert np.array_equal(to_f64(scales.float())[:, 0], s.astype(np.float64))
+    assert symmetric or np.array_equal(zeros.cpu().numpy()[:, 0], z)
+    want = np.clip(np.rint(w / s[:, None]) + z[:, None], 0, 15)
+    assert np.array_equal(int4_ref.unpack(codes.cpu().numpy()), want)
+
+
 def test_codec_three_dimensions_empty_and_streams():
     import torch
 
@@ -261,6 +287,55 @@ def test_dense_swiglu():
         assert np.array_equal(to_f64(lin.forward(bf16(x), i, dtype=torch.float32))[:, 0], got)
 
 
+# More rows of weights: other divisions of the work among workgroups and waves, with
+# last tiles that fill no group of them.
+@pytest.mark.parametrize("T,N,K,group,swiglu", [
+    (3, 9000, 96, 32, False), (7, 8233, 128, 128, False), (12, 9001, 192, 64, False), (2, 24650, 64, 64, False),
+    (8, 24645, 128, 128, False), (9, 24650, 96, 32, False), (5, 8200, 8256, 64, False), (13, 8199, 8192, 128, False),
+    (33, 5490, 160, 32, False), (128, 2130, 384, 128, False), (100, 2129, 320, 64, False),
+    (4, 8800, 96, 32, True), (16, 24660, 64, 64, True), (6, 8260, 8224, 32, True), (128, 2200, 256, 128, True),
+    (47, 7000, 96, 32, True)])
+def test_dense_of_many_rows(T, N, K, group, swiglu):
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    rng = np.random.default_rng(T + N + K)
+    q, s, z, w = integers(rng, 1, N, K, group)
+    x = ints(rng, (T, K))
+    y = x @ int4_ref.values(q[0], s[0], z[0]).T
+    got = cm.Int4Linear(*(t[0] for t in w), swiglu=swiglu).forward(bf16(x), dtype=torch.float32)
+    if swiglu:
+        want, tol = int4_ref.swiglu(y, np.zeros_like(y))
+        assert (np.abs(to_f64(got) - want) <= tol + 1e-35).all()
+    else:
+        exact_equal(got, y)
+
+
+@pytest.mark.parametrize("kind", ["distinct", "mixed", "one"])
+@pytest.mark.parametrize("T,k,E,N,K,group", [(4, 2, 3, 8200, 64, 64), (10, 1, 3, 8202, 96, 32), (16, 2, 3, 8230, 128, 128),
+                                             (100, 1, 30, 70, 256, 128), (100, 1, 100, 66, 128, 64), (90, 1, 3, 8200, 32, 32),
+                                             (64, 2, 4, 4140, 64, 64), (16, 2, 40, 530, 128, 128), (33, 2, 3, 9010, 32, 32)])
+def test_experts_of_many_rows(T, k, E, N, K, group, kind):
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    rng = np.random.default_rng(T * k + N + K)
+    q, s, z, w = integers(rng, E, N, K, group)
+    ids = some_ids(rng, T, k, E, kind)
+    x, weights = ints(rng, (T, K)), 2.0 ** rng.integers(-2, 2, (T, k))
+    by_expert = [x @ int4_ref.values(q[e], s[e], z[e]).T for e in range(E)]
+    y = np.array([[by_expert[e][t] if 0 <= e < E else np.zeros(N) for e in ids[t]] for t in range(T)])
+    i, p = torch.from_numpy(ids).cuda(), torch.from_numpy(weights).float().cuda()
+    lin = cm.Int4Linear(*w)
+    exact_equal(lin.forward(bf16(x), i, dtype=torch.float32), y)
+    exact_equal(lin.forward(bf16(x), i, p, dtype=torch.float32), (y * weights[:, :, None]).sum(axis=1))
+    want, tol = int4_ref.swiglu(y, np.zeros_like(y))
+    got = to_f64(cm.Int4Linear(*w, swiglu=True).forward(bf16(x), i, dtype=torch.float32))
+    assert (np.abs(got - want) <= tol + 1e-35).all()
+
+
 @pytest.mark.parametrize("T,k,E,N,K,group", [(1, 1, 1, 512, 4096, 128), (33, 1, 1, 130, 2080, 32), (7, 2, 8, 96, 14336, 128),
                                              (16, 4, 32, 256, 2048, 64), (64, 2, 4, 64, 1024, 256)])
 def test_normal_values(T, k, E, N, K, group):
@@ -289,6 +364,23 @@ def test_normal_values(T, k, E, N, K, group):
                                  (glu.forward(x, i, dtype=dtype), gl, gtol)):
                 assert got.dtype == dtype
                 assert (np.abs(to_f64(got) - want) <= t + half * (np.abs(want) + t) + 1e-35).all()
+
+
+def test_gates_beyond_the_largest_float():
+    """A gate of -infinity (its fp32 sum overflows) closes: its exact SiLU rounds to -0."""
+    import torch
+
+    import sparse_moe_gemm_amd as cm
+
+    codes = torch.full((32, 64), 0x00, dtype=torch.uint8, device="cuda")
+    codes[16:] = 0x99  # up: 1 each
+    scales = torch.ones(32, 1, dtype=torch.bfloat16, device="cuda")
+    scales[:8] = 2.0 ** 120
+    lin = cm.Int4Linear(codes, scales, swiglu=True)
+    for T in (1, 7, 40):
+        y = lin.forward(bf16(np.ones((T, 128))), dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert (y == 0).all() and y.shape == (T, 16)
 
 
 def test_rows_do_not_reach_each_other():
