@@ -35,8 +35,8 @@ constexpr int kMaxRows = kInt4Rows;
 
 __host__ __device__ __forceinline__ int units_of(int K) { return (K + kUnitK - 1) / kUnitK; }
 
-// Tiles of 16 rows, an even number (a work item takes one or two). SwiGLU: gate
-// and up tiles of the same 16 columns in turn.
+// Tiles of 16 rows, an even number (a work item takes one, two or four). SwiGLU:
+// gate and up tiles of the same 16 columns in turn.
 __host__ __device__ __forceinline__ int tiles_of(int N, int swiglu)
 {
     return swiglu ? 2 * ((N / 2 + 15) / 16) : ((N + 15) / 16 + 1) / 2 * 2;
