@@ -478,10 +478,11 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
         for t in (x, weight, residual, y, residual_out):
             if t is not None:
                 t.record_stream(stream)
+    like = stream is None and x.is_contiguous()  # the cheaper allocation
     if with_y and y is None:
-        y = empty((T, d), x.dtype)
+        y = torch.empty_like(x) if like else empty((T, d), x.dtype)
     if residual is not None and residual_out is None:
-        residual_out = empty((T, d), x.dtype)
+        residual_out = torch.empty_like(x) if like else empty((T, d), x.dtype)
     codes = scales = None
     if quantize is not None:
         codes, scales = empty((T, d), torch.uint8), empty((T,), torch.float32)
