@@ -11,9 +11,8 @@
 // infinity or NaN gets the scale NaN. rint rounds ties to even. Reading back
 // rounds (q - z) * s once (exact in fp32).
 //
-// Both directions move each byte once: 14336 x 4096 bf16, groups of 128: 147 MB
-// in 36 us one way (read 4 : write 1; its divisions share the time) and 25 us
-// (5.9 TB/s) the other.
+// Both directions move each byte once: 14336 x 4096 bf16, groups of 128: 148 MB
+// in 27.9 us one way (5.3 TB/s) and 25.3 us (5.8 TB/s) the other.
 #include "common.hpp"
 
 namespace cmoe {
@@ -88,7 +87,8 @@ template <int L>
 __device__ __forceinline__ void join(Range& r)
 {
     join_step<0xB1>(r);  // quad_perm [1,0,3,2]
-    join_step<0x4E>(r);  // quad_perm [2,3,0,1]
+    if constexpr (L >= 4)
+        join_step<0x4E>(r);  // quad_perm [2,3,0,1]
     if constexpr (L >= 8)
         join_step<0x141>(r);  // row_half_mirror
     if constexpr (L == 16)
@@ -105,7 +105,7 @@ struct Group {
 // v / s by the reciprocal and one correction, q + (v - q s) / s: the nearest
 // float, as a division gives (v has 24 bits and s 8: a quotient is at least
 // 2^-33 of itself away from every midpoint, and the correction is good to
-// 2^-45), at a third of its cost: 14336 x 4096 in groups of 128 54 -> 36 us, 4.0 TB/s.
+// 2^-45), at a third of its cost: 14336 x 4096 in groups of 128 54.6 -> 44.2 us.
 // |s| within 2^+-100, so that nothing underflows that a rounding to an integer
 // could see.
 __device__ __forceinline__ float quotient(float v, const Group& g)
@@ -162,24 +162,29 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], const Group& g)
     return g.flat ? 0x11111111u * (uint32_t)g.z : even | odd << 4;
 }
 
-// L neighbouring lanes share a group of 8 * L * m values, lane j of them holding
-// values 8j .. +8 of each of its m parts: a wave reads whole lines and writes
-// 256 bytes of codes. Groups of ONE part stay in registers between the two
-// steps, longer ones are read again. Four groups per thread are in flight.
-template <typename T, bool VEC, int L, bool ONE>
+// L neighbouring lanes share a group of 8 L P m values, lane j of them holding
+// values 8j .. +8 of its parts of 8 L. What a group costs beside its values (the
+// range's exchange, scale and zero point) is thus shared by 16 or 32 values per
+// lane; with 8 the instructions took longer than the memory (14336 x 4096, groups
+// of 128: 16 lanes 36.0 us, 4 lanes 27.9; of 32, both ways: 4 lanes 59.9, 2 lanes 54.9, one,
+// whose loads no longer share lines, 60.8). m = 1: the values stay in registers
+// between the two steps, other groups are read again (of 256 so, both ways: 87.5 us,
+// in registers 52.3).
+// 32 values per thread are in flight.
+template <typename T, bool VEC, int L, int P, bool ONE>
 __global__ __launch_bounds__(kThreads) void int4_quantize_kernel(const T* w, int64_t groups, int per_row, int m,
                                                                  int64_t ld, uint32_t* codes, uint16_t* scales,
                                                                  uint8_t* zeros)
 {
-    constexpr int kFlight = 4;
+    constexpr int kFlight = 4 / P, kPart = 8 * L;
     const int j = threadIdx.x % L;
-    const int group = ONE ? 8 * L : 8 * L * m;
+    const int parts = ONE ? P : P * m, group = kPart * parts;
     const int64_t step = (int64_t)gridDim.x * (kThreads / L);
     const int64_t first = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const bool dense = ld == (int64_t)per_row * group;  // rows without gaps
     for (int64_t g0 = first; g0 < groups; g0 += step * kFlight) {
         const T* src[kFlight];
-        float v[kFlight][8];
+        float v[kFlight][P][8];
         Range r[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
@@ -192,16 +197,24 @@ __global__ __launch_bounds__(kThreads) void int4_quantize_kernel(const T* w, int
         }
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
-            load8<VEC>(src[f], v[f]);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                load8<VEC>(src[f] + p * kPart, v[f][p]);
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
-            widen(r[f], v[f]);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                widen(r[f], v[f][p]);
         if constexpr (!ONE)
-            for (int p = 1; p < m; ++p)
+            for (int p = P; p < parts; p += P)
 #pragma unroll
                 for (int f = 0; f < kFlight; ++f) {
-                    load8<VEC>(src[f] + p * 8 * L, v[f]);
-                    widen(r[f], v[f]);
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        load8<VEC>(src[f] + (p + q) * kPart, v[f][q]);
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        widen(r[f], v[f][q]);
                 }
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
@@ -210,14 +223,18 @@ __global__ __launch_bounds__(kThreads) void int4_quantize_kernel(const T* w, int
             if (g >= groups)
                 break;  // no exchange between lanes is left
             const Group q = group_of(r[f], zeros == nullptr);
-            if constexpr (ONE)
-                codes[g * L + j] = encode8(v[f], q);
-            else
-                for (int p = 0; p < m; ++p) {
+            uint32_t* out = codes + g * (L * parts) + j;
+            if constexpr (ONE) {
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    out[p * L] = encode8(v[f][p], q);
+            } else {
+                for (int p = 0; p < parts; ++p) {
                     float u[8];
-                    load8<VEC>(src[f] + p * 8 * L, u);
-                    codes[(g * m + p) * L + j] = encode8(u, q);
+                    load8<VEC>(src[f] + p * kPart, u);
+                    out[p * L] = encode8(u, q);
                 }
+            }
             if (j == 0) {
                 scales[g] = q.bits;
                 if (zeros)
@@ -276,20 +293,19 @@ hipError_t launch_quantize(const T* w, int64_t rows, int64_t cols, int64_t ld, i
                            uint16_t* scales, uint8_t* zeros, hipStream_t s)
 {
     const int64_t groups = rows * (cols / group);
-    const int lanes = group >= 128 ? 16 : group / 8;
-    const int64_t blocks = std::min<int64_t>((groups + 4 * (kThreads / lanes) - 1) / (4 * (kThreads / lanes)), 16384);
-    auto go = [&](auto kern, int m) {
+    auto go = [&](auto kern, int m, int L, int flight) {
+        const int64_t blocks = std::min<int64_t>((groups + flight * (kThreads / L) - 1) / (flight * (kThreads / L)), 16384);
         hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kThreads), 0, s, w, groups, (int)(cols / group), m, ld,
                            (uint32_t*)codes, scales, zeros);
     };
-    if (group == 32)
-        go(int4_quantize_kernel<T, VEC, 4, true>, 1);
-    else if (group == 64)
-        go(int4_quantize_kernel<T, VEC, 8, true>, 1);
-    else if (group == 128)
-        go(int4_quantize_kernel<T, VEC, 16, true>, 1);
-    else
-        go(int4_quantize_kernel<T, VEC, 16, false>, group / 128);
+    switch (group) {
+    case 32: go(int4_quantize_kernel<T, VEC, 2, 2, true>, 1, 2, 2); break;
+    case 64: go(int4_quantize_kernel<T, VEC, 2, 4, true>, 1, 2, 1); break;
+    case 128: go(int4_quantize_kernel<T, VEC, 4, 4, true>, 1, 4, 1); break;
+    case 256: go(int4_quantize_kernel<T, VEC, 8, 4, true>, 1, 8, 1); break;
+    case 512: go(int4_quantize_kernel<T, VEC, 16, 4, true>, 1, 16, 1); break;
+    default: go(int4_quantize_kernel<T, VEC, 4, 4, false>, group / 128, 4, 1);
+    }
     return hipGetLastError();
 }
 

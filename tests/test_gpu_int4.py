@@ -49,7 +49,7 @@ def check_codec(t, group, symmetric, few_unsure=True):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,group", [(1, 32, 32), (3, 64, 64), (5, 96, 32), (7, 128, 128), (33, 2080, 32),
                                              (64, 1536, 64), (129, 1024, 128), (9, 1024, 256), (4, 768, 768),
-                                             (2, 16384, 1024), (1025, 384, 128)])
+                                             (2, 16384, 1024), (1025, 384, 128), (67, 1536, 512), (131, 512, 256), (3, 1920, 640)])
 def test_codec(rows, cols, group, dtype, symmetric):
     import torch
 
