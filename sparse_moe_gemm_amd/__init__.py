@@ -661,7 +661,7 @@ class Int4Linear:
         with swiglu) their weighted sum [T][n]; n is N, or N/2 with swiglu. A slot
         whose id is outside 0..E-1 gives zeros and adds nothing. At most
         INT4_ROWS (128) rows T * k. y bf16, or dtype=torch.float32; a given y is
-        written and returned. The work is enqueued on `stream`, by default the
+        written and returned, and may not overlap x. The work is enqueued on `stream`, by default the
         current one; a given stream must already be ordered behind the work
         that makes the tensors."""
         import torch
