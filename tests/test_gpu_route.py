@@ -64,7 +64,9 @@ def test_plain_rules(E, k, rule):
 @pytest.mark.parametrize("score", ["max", "top2"])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups,top,k", [(256, 8, 4, 8), (256, 8, 1, 8), (16, 16, 3, 3), (160, 8, 3, 6), (60, 4, 2, 4),
-                                            (64, 64, 8, 8), (128, 64, 5, 8), (255, 5, 2, 7), (12, 3, 1, 4), (192, 2, 1, 8)])
+                                            (64, 64, 8, 8), (128, 64, 5, 8), (255, 5, 2, 7), (12, 3, 1, 4), (192, 2, 1, 8),
+                                            (64, 4, 2, 6), (256, 2, 1, 8), (128, 2, 1, 5), (128, 4, 3, 8), (24, 3, 2, 3),
+                                            (40, 5, 3, 8), (256, 4, 1, 8), (250, 10, 7, 8)])
 def test_groups(E, groups, top, k, scoring, score):
     for bias in (None, np.random.default_rng(E).normal(0, 0.05, E).astype(np.float32)):
         check(logits_of(70, E, E + top), k, bias, scoring=scoring, groups=groups, top_groups=top, group_score=score)
