@@ -591,10 +591,11 @@ def _int4_group(codes, scales, zeros):
 
 def dequantize_int4(codes, scales, zeros=None, dtype=None, stream=None):
     """The values [..][K] (bf16 by default, rounded; or fp32, exact) of 4-bit
-    groups as quantize_int4 gives them (scales bf16 or fp16; without zeros every
-    zero point is 8): what MoELayer takes for such weights. The work is
-    enqueued on `stream`, by default the current one; a given stream must
-    already be ordered behind the work that makes the tensors."""
+    groups as quantize_int4 gives them (scales bf16 or fp16; of a zero point's
+    byte the low four bits count, without zeros every zero point is 8): what
+    MoELayer takes for such weights. The work is enqueued on `stream`, by
+    default the current one; a given stream must already be ordered behind the
+    work that makes the tensors."""
     import torch
 
     group = _int4_group(codes, scales, zeros)

@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kThreads) void int4_dequantize_kernel(const uint32_
             const int64_t g = (units >> 32) == 0 ? (uint32_t)u / (uint32_t)per_group : u / per_group;
             c[f] = codes[u];
             sb[f] = scales[g];
-            z[f] = zeros ? (float)zeros[g] : 8.0f;
+            z[f] = zeros ? (float)(zeros[g] & 15) : 8.0f;  // as int4_pack_kernel reads them
         }
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
