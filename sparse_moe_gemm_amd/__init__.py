@@ -233,6 +233,9 @@ def _empty_on(stream, device):
     return empty
 
 
+_I32_MAX = (1 << 31) - 1  # ctypes would cut a larger size, and the library answer for another one
+
+
 def quantize_fp8(w, stream=None):
     """(codes uint8 [rows][cols], scales fp32 [rows]) of a contiguous bf16
     device tensor [rows][cols]: the 8-bit codes a layer built with
@@ -350,8 +353,11 @@ class RoutingRule:
             raise ValueError('scoring must be "softmax" or "sigmoid"')
         if group_score not in ("max", "top2"):
             raise ValueError('group_score must be "max" or "top2"')
-        self.c = Rule(int(scoring == "sigmoid"), groups, groups if top_groups is None else top_groups,
-                      int(group_score == "top2"), int(bool(normalize)), scale)
+        top_groups = groups if top_groups is None else top_groups
+        if max(abs(groups), abs(top_groups)) > _I32_MAX:
+            raise ValueError("at most 64 groups")
+        self.c = Rule(int(scoring == "sigmoid"), groups, top_groups, int(group_score == "top2"), int(bool(normalize)),
+                      scale)
 
 
 _default_rule = RoutingRule()
@@ -383,6 +389,8 @@ def route(logits, top_k, rule: RoutingRule | None = None, bias=None, stream=None
     if not (bf16 or logits.dtype == torch.float32) or logits.dim() != 2 or not logits.is_cuda:
         raise TypeError("logits must be a 2-D bfloat16 or float32 device tensor")
     T, E = logits.shape
+    if T > _I32_MAX or E > _I32_MAX or top_k > _I32_MAX:
+        raise ColibriError("colibri_moe_route", ERR_INVALID_ARG)
     row_stride, step = logits.stride()
     if (E > 1 and step != 1) or (T > 1 and row_stride < E):
         raise ValueError("rows must be contiguous and must not overlap")
@@ -451,6 +459,8 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
     if not (bf16 or x.dtype == torch.float32) or x.dim() != 2 or not x.is_cuda:
         raise TypeError("x must be a 2-D bfloat16 or float32 device tensor")
     T, d = x.shape
+    if d > _I32_MAX:
+        raise ColibriError("colibri_moe_rms_norm", ERR_INVALID_ARG)
     x_stride = _row_stride(x, "x")
     w_bf16 = weight.dtype == torch.bfloat16
     if not (w_bf16 and bf16 or weight.dtype == torch.float32) or weight.device != x.device or weight.dim() != 1:
@@ -639,8 +649,10 @@ class Int4Linear:
         self.E, self.N, self.K, self.group = (1 if len(lead) == 1 else lead[0]), lead[-1], half * 2, group
         self.swiglu, self.device = bool(swiglu), codes.device
         self.out_features = self.N // 2 if swiglu else self.N
-        self.c = Int4(self.E, self.N, self.K, group, BF16 if scales.dtype == torch.bfloat16 else F16, int(self.swiglu))
-        n = colibri_moe_int4_bytes(self.c)
+        n = -1
+        if max(self.E, self.N, self.K) <= _I32_MAX:
+            self.c = Int4(self.E, self.N, self.K, group, BF16 if scales.dtype == torch.bfloat16 else F16, int(self.swiglu))
+            n = colibri_moe_int4_bytes(self.c)
         if n < 0:
             raise ValueError("not supported: K must be a multiple of 32, group 32, 64 or a multiple of 128, E at most 256, "
                              "N even with swiglu")
@@ -763,6 +775,8 @@ class MoELayer:
         f = w_gate.shape[1]
         self.d, self.E, self.f, self.k, self.max_tokens = d, E, f, int(top_k), int(max_tokens)
         self.dtype = dt
+        if max(d, f, E, abs(self.k), abs(self.max_tokens)) > _I32_MAX:
+            raise ColibriError("colibri_moe_init", ERR_INVALID_ARG)
         self.cfg = Config(d, f, E, self.k, self.max_tokens, BF16 if dt == torch.bfloat16 else F32, flags)
         for t in (w_router, w_gate, w_up, w_down):
             if not t.is_cuda or not t.is_contiguous() or t.dtype != dt or t.device != w_router.device:
