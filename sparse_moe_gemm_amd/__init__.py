@@ -498,6 +498,9 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
         codes, scales = empty((T, d), torch.uint8), empty((T,), torch.float32)
     out = Normed(y, residual_out, codes, scales)
     if T == 0 or d == 0:
+        if T > 0 and scales is not None:  # rows of no values have the scale of rows of zeros
+            with torch.cuda.stream(stream):  # None: where we are
+                scales.fill_(1.0)
         return out
     n = Norm(x.data_ptr(), x_stride, None if residual is None else residual.data_ptr(), r_stride, weight.data_ptr(),
              BF16 if bf16 else F32, BF16 if w_bf16 else F32, T, d, eps, None if y is None else y.data_ptr(),
