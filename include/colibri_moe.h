@@ -314,9 +314,9 @@ colibri_moe_status_t colibri_moe_route(const void* logits, colibri_moe_dtype_t d
  * rows x cols values; row t of x, residual and residual_out starts at element
  * t * their stride (at least cols); y, codes [rows][cols] and scales [rows] are
  * dense. residual, residual_out, y and codes (with scales) may be NULL, but not
- * all outputs. residual_out may be residual and y may be x (with the same
- * stride); other overlaps are not allowed. Pointers aligned to their type
- * (ALIGNMENT); rows >= 0 (0: nothing to do), 1 <= cols <= 2^24, rows * stride <=
+ * all outputs. y and residual_out may each take the rows of x or of residual
+ * (the same address and stride); otherwise no output may overlap an input or
+ * another output (INVALID_ARG). Pointers aligned to their type (ALIGNMENT); rows >= 0 (0: nothing to do), 1 <= cols <= 2^24, rows * stride <=
  * 2^42, eps > 0, finite; INVALID_ARG otherwise. Caller-owned DEVICE buffers.
  * Enqueues on hip_stream (NULL = default stream) and returns without waiting.
  * Needs no handle. */

@@ -449,8 +449,8 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quantize=None, with_y=True, y=N
     Normed(y, residual, codes, scales) with residual = x + residual. quantize
     "fp8" also gives y's E4M3 codes (uint8) and power-of-two row scales, in
     quantize_fp8's format, from the unrounded values; with_y=False leaves y out.
-    Given outputs y (contiguous; may be x) and residual_out (may be residual) are
-    written and returned. The work is enqueued on `stream`, by default the
+    Given outputs y (contiguous) and residual_out are written and returned; each
+    may be x or residual itself, and may not overlap anything else. The work is enqueued on `stream`, by default the
     current one; a given stream must already be ordered behind the work that
     makes the tensors."""
     import torch

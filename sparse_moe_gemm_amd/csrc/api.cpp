@@ -262,6 +262,49 @@ bool int4_fits(const colibri_moe_int4_t& m)
            (m.swiglu == 0 || (m.swiglu == 1 && m.rows % 2 == 0));
 }
 
+// A buffer of n rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+    int64_t at, n, pitch, width;
+    Rows(const void* p, int64_t rows, int64_t row_pitch, int64_t row_width)
+        : at((int64_t)(uintptr_t)p), n(p ? rows : 0), pitch(row_pitch), width(row_width)
+    {
+        if (pitch == width && n > 1) {  // one row
+            width *= n;
+            n = 1;
+        }
+    }
+    int64_t row(int64_t i) const { return at + i * pitch; }
+    // First of its rows that ends behind address p.
+    int64_t behind(int64_t p) const { return p < at + width ? 0 : n > 1 ? (p - at - width) / pitch + 1 : 1; }
+};
+
+// Whether some row of a and some of b share a byte.
+bool rows_meet(const Rows& a, const Rows& b)
+{
+    if (a.n == 0 || b.n == 0 || a.row(a.n - 1) + a.width <= b.at || b.row(b.n - 1) + b.width <= a.at)
+        return false;
+    if (a.n > 1 && b.n > 1 && a.pitch == b.pitch) {
+        // rows i and i + m meet where b.at - a.at + m * pitch lies within (-b.width, a.width)
+        const int64_t d = b.at - a.at, low = -b.width - d;
+        int64_t m = low >= 0 ? low / a.pitch + 1 : -((-low - 1) / a.pitch);  // the least such m
+        m = std::max(m, 1 - a.n);
+        return m < b.n && d + m * a.pitch < a.width;
+    }
+    for (int64_t i = a.behind(b.at), j = 0; i < a.n;) {
+        j = b.behind(a.row(i));
+        if (j >= b.n)
+            return false;
+        if (b.row(j) < a.row(i) + a.width)
+            return true;
+        i = a.behind(b.row(j));
+    }
+    return false;
+}
+
+// Whether a and b start at the same address and, if they have several rows,
+// go on alike.
+bool same_rows(const Rows& a, const Rows& b) { return a.at == b.at && a.n == b.n && (a.n <= 1 || a.pitch == b.pitch); }
+
 // Compute units of the current device; 0 if it cannot be asked.
 int current_cus()
 {
@@ -947,6 +990,24 @@ colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip
     if ((((uintptr_t)n->x | (uintptr_t)n->residual | (uintptr_t)n->y | (uintptr_t)n->residual_out) & mask) ||
         ((uintptr_t)n->weight & (n->weight_dtype == COLIBRI_MOE_BF16 ? 1u : 3u)) || ((uintptr_t)n->scales & 3u))
         return COLIBRI_MOE_ERR_ALIGNMENT;
+    // Every value of a row is read before the first of it is written, so y and
+    // residual_out may take an input's rows. Nothing else may overlap an output.
+    const int64_t es = n->dtype == COLIBRI_MOE_BF16 ? 2 : 4, wes = n->weight_dtype == COLIBRI_MOE_BF16 ? 2 : 4;
+    const auto rows = [&](const void* p, int64_t stride, int64_t size) {
+        return Rows(p, n->rows, stride * size, n->cols * size);
+    };
+    const Rows in[3] = {rows(n->x, n->x_stride, es), rows(n->residual, n->residual_stride, es),
+                        Rows(n->weight, 1, 0, n->cols * wes)};
+    const Rows out[4] = {rows(n->y, n->cols, es), rows(n->residual_out, n->residual_out_stride, es),
+                         rows(n->codes, n->cols, 1), Rows(n->codes ? n->scales : nullptr, n->rows, 4, 4)};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 3; ++i)
+            if (rows_meet(out[o], in[i]) && !(o < 2 && i < 2 && same_rows(out[o], in[i])))
+                return COLIBRI_MOE_ERR_INVALID_ARG;
+        for (int p = 0; p < o; ++p)
+            if (rows_meet(out[o], out[p]))
+                return COLIBRI_MOE_ERR_INVALID_ARG;
+    }
     const NormArgs a{n->x, n->x_stride, n->residual, n->residual_stride, n->weight, n->dtype == COLIBRI_MOE_BF16,
                      n->weight_dtype == COLIBRI_MOE_BF16, n->rows, n->cols, n->eps, n->y, n->residual_out,
                      n->residual_out_stride, n->codes, n->scales};

@@ -170,7 +170,7 @@ __device__ __forceinline__ float row_max(float v, float* red)
 // ones another lane holds too: they are left out of the sum and written twice,
 // with the same bits. All of a row's loads are unconditional and in flight
 // together (lanes behind the row read its end). Every value is read before the
-// first one is written, so y may be x and the residual's sum the residual.
+// first one is written, so y and the sum may take the place of x or the residual.
 template <typename T, int NC, int WPR>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a)
 {
