@@ -391,7 +391,8 @@ colibri_moe_status_t colibri_moe_int4_pack(const colibri_moe_int4_t* m, const ui
  *   ids [T][k]: y[t][j] = W[ids[t][j]] x[t], or of x[t][j] with x_per_slot (x [T][k][K]);
  *   with swiglu, of each row's N values g (first half) and u: SiLU(g) * u, N/2 values;
  *   with weights [T][k] (not with swiglu): y[t] = sum_j weights[t][j] W[ids[t][j]] x.
- * x bf16, y bf16 or fp32 (y_dtype), dense, not overlapping (INVALID_ARG). An id
+ * x bf16, y bf16 or fp32 (y_dtype), dense; y may overlap neither x, ids, weights
+ * nor packed (INVALID_ARG). An id
  * outside 0..n_experts-1 marks a slot without an expert: its row of y is 0, and
  * it adds nothing to a weighted sum. Ids may repeat. Weights enter the products unrounded; sums are fp32, in
  * an order that the call's sizes and ids decide (the same call gives the same

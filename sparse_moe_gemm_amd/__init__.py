@@ -677,9 +677,9 @@ class Int4Linear:
         with swiglu) their weighted sum [T][n]; n is N, or N/2 with swiglu. A slot
         whose id is outside 0..E-1 gives zeros and adds nothing. At most
         INT4_ROWS (128) rows T * k. y bf16, or dtype=torch.float32; a given y is
-        written and returned, and may not overlap x. The work is enqueued on `stream`, by default the
-        current one; a given stream must already be ordered behind the work
-        that makes the tensors."""
+        written and returned, and may not overlap x, ids or weights. The work is
+        enqueued on `stream`, by default the current one; a given stream must
+        already be ordered behind the work that makes the tensors."""
         import torch
 
         if (x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != self.device or x.dim() not in (2, 3)

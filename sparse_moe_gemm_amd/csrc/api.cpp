@@ -1085,11 +1085,13 @@ colibri_moe_status_t colibri_moe_int4_linear(const colibri_moe_int4_t* m, const 
     if (!aligned16(packed) || !aligned16(x) || ((uintptr_t)ids & 3u) || ((uintptr_t)weights & 3u) ||
         ((uintptr_t)y & (y_dtype == COLIBRI_MOE_BF16 ? 1u : 3u)))
         return COLIBRI_MOE_ERR_ALIGNMENT;
-    // workgroups write y while others still read x
-    const int64_t x_bytes = (int64_t)(x_per_slot ? T * k : T) * m->cols * 2;
-    const int64_t y_bytes = (int64_t)(ids && !weights ? T * k : T) * (m->swiglu ? m->rows / 2 : m->rows) *
-                            (y_dtype == COLIBRI_MOE_BF16 ? 2 : 4);
-    if ((const uint8_t*)x < (const uint8_t*)y + y_bytes && (const uint8_t*)y < (const uint8_t*)x + x_bytes)
+    // workgroups write y while others still read the rest
+    const auto span = [](const void* p, int64_t bytes) { return Rows(p, 1, 0, bytes); };
+    const Rows out = span(y, (int64_t)(ids && !weights ? T * k : T) * (m->swiglu ? m->rows / 2 : m->rows) *
+                                 (y_dtype == COLIBRI_MOE_BF16 ? 2 : 4));
+    if (rows_meet(out, span(x, (int64_t)(x_per_slot ? T * k : T) * m->cols * 2)) ||
+        rows_meet(out, span(ids, (int64_t)T * k * 4)) || rows_meet(out, span(weights, (int64_t)T * k * 4)) ||
+        rows_meet(out, span(packed, colibri_moe_int4_bytes(m))))
         return COLIBRI_MOE_ERR_INVALID_ARG;
     const int cus = current_cus();
     if (cus <= 0)

@@ -1,6 +1,7 @@
 """Buffers of one call that overlap, without a GPU (tests/fake_hip.c stands in for the
 runtime and runs nothing): rms_norm takes outputs in an input's place and refuses
-every other overlap, against the sets of bytes themselves."""
+every other overlap, against the sets of bytes themselves; int4_linear takes no y that
+overlaps what it reads."""
 import os
 import subprocess
 import sys
@@ -87,6 +88,29 @@ assert call(n, d, cm.BF16, {"x": row, "y": (P + n * 4 * d - 2 * d - 2, d)}, weig
 """
 
 
+LINEAR = SETUP + """
+m = cm.Int4(4, 64, 256, 128, cm.BF16, 0)  # y [4][2][64] bf16: 1024 bytes
+SIZES = dict(packed=cm.colibri_moe_int4_bytes(m), x=2048, ids=32, weights=32)
+
+def call(y, summed=False, **at):
+    fake.fake_clear()
+    p = {n: 0x1000000 * (i + 2) for i, n in enumerate(SIZES)}
+    p.update(at)
+    return cm.colibri_moe_int4_linear(m, p["packed"], p["x"], 4, 2, 0, p["ids"], p["weights"] if summed else None, y,
+                                      cm.BF16)
+
+for name, size in SIZES.items():
+    for summed in (False, True):
+        if name == "weights" and not summed:
+            continue
+        wide = 512 if summed else 1024
+        for at, want in ((P, cm.ERR_INVALID_ARG), (P + wide - 16, cm.ERR_INVALID_ARG), (P + wide, cm.OK),
+                         (P - size + 16, cm.ERR_INVALID_ARG), (P - size, cm.OK)):
+            assert call(P, summed, **{name: at}) == want, (name, summed, at - P)
+print("done")
+"""
+
+
 @pytest.fixture(scope="module")
 def fake(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("fake") / "libfakehip.so")
@@ -105,3 +129,7 @@ def child(fake, program):
 def test_rms_norm(fake):
     _, taken, refused = child(fake, NORM).split()
     assert int(taken) > 5000 and int(refused) > 5000
+
+
+def test_int4_linear(fake):
+    assert child(fake, LINEAR).split() == ["done"]
