@@ -666,8 +666,9 @@ class Int4Linear:
             for t in (codes, scales, zeros):
                 if t is not None:
                     t.record_stream(stream)
+        self._home = _stream_of(codes, stream)  # whose pool packed is of
         st = _on_device_of(codes, colibri_moe_int4_pack, self.c, codes.data_ptr(), scales.data_ptr(),
-                           None if zeros is None else zeros.data_ptr(), self.packed.data_ptr(), _stream_of(codes, stream))
+                           None if zeros is None else zeros.data_ptr(), self.packed.data_ptr(), self._home)
         if st != OK:
             raise ColibriError("colibri_moe_int4_pack", st)
 
@@ -712,15 +713,18 @@ class Int4Linear:
             raise ColibriError("colibri_moe_int4_linear", ERR_TOO_LARGE)
         if stream is not None:
             _check_stream(stream, self.device)
-            for t in (x, ids, weights, y, self.packed):
+            for t in (x, ids, weights, y):
                 if t is not None:
                     t.record_stream(stream)
+        on = _stream_of(x, stream)
+        if on != self._home:  # packed is not used again before this stream is done with it
+            self.packed.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
         if y is None:
             y = (torch.empty(shape, dtype=value, device=self.device) if stream is None
                  else _empty_on(stream, self.device)(shape, value))
         st = _on_device_of(x, colibri_moe_int4_linear, self.c, self.packed.data_ptr(), x.data_ptr(), T, k, int(per_slot),
                            None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(),
-                           y.data_ptr(), F32 if f32 else BF16, _stream_of(x, stream))
+                           y.data_ptr(), F32 if f32 else BF16, on)
         if st != OK:
             raise ColibriError("colibri_moe_int4_linear", st)
         return y
