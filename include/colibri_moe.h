@@ -298,7 +298,8 @@ colibri_moe_status_t colibri_moe_dequantize_mxfp4(const uint8_t* codes, const ui
  * element t * row_stride, aligned to their type): ids and weights [T][k], 4-byte
  * aligned. E <= 256, k <= min(8, E), row_stride >= E, T >= 0 (0: nothing to do),
  * T * row_stride <= 2^42; INVALID_ARG otherwise, UNSUPPORTED for more experts or
- * a larger k. bias as for colibri_moe_init_rule. Caller-owned DEVICE buffers.
+ * a larger k. bias as for colibri_moe_init_rule. Caller-owned DEVICE buffers
+ * that do not overlap.
  * Enqueues on hip_stream (NULL = default stream) and returns without waiting.
  * Needs no handle. */
 colibri_moe_status_t colibri_moe_route(const void* logits, colibri_moe_dtype_t dtype, int64_t row_stride, int32_t T,
@@ -349,8 +350,8 @@ colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip
  *
  * colibri_moe_quantize_int4 makes them from w [rows][cols], bf16 or fp32, row r
  * starting at element r * row_stride, with bf16 scales. With lo = min(0, the
- * group's least value) and hi = max(0, its greatest): s = (hi - lo) / 15 rounded to
- * bf16, z = -lo / s and q = w / s + z, both rounded to nearest (ties to even) before
+ * group's least value) and hi = max(0, its greatest), in fp32: s = (hi - lo) / 15
+ * rounded to bf16, z = -lo / s and q = w / s + z, both rounded to nearest (ties to even) before
  * the sum and clamped to 0..15; zeros NULL: s = max |w| / 7 rounded to bf16,
  * z = 8. Where s rounds to 0 the group is zeros (s = 1); an infinity or NaN in
  * a group makes its scale NaN.
@@ -358,10 +359,11 @@ colibri_moe_status_t colibri_moe_rms_norm(const colibri_moe_norm_t* n, void* hip
  * colibri_moe_dequantize_int4 gives the values back, bf16 (rounded) or fp32
  * (exact), from bf16 or fp16 scales: what a layer's init takes.
  *
- * Caller-owned DEVICE buffers, w, scales and zeros aligned to their type, codes
- * 4 bytes, out 16. rows >= 1, rows * cols <= 2^40, rows * row_stride <= 2^42,
- * row_stride >= cols; otherwise INVALID_ARG. Both enqueue on hip_stream (NULL =
- * default stream) and return without waiting. They need no handle. */
+ * Caller-owned DEVICE buffers that do not overlap, w, scales and zeros aligned to
+ * their type, codes 4 bytes, out 16. rows >= 1, rows * cols <= 2^40, rows *
+ * row_stride <= 2^42, row_stride >= cols; otherwise INVALID_ARG. Both enqueue on
+ * hip_stream (NULL = default stream) and return without waiting. They need no
+ * handle. */
 colibri_moe_status_t colibri_moe_quantize_int4(const void* w, colibri_moe_dtype_t dtype, int64_t rows, int64_t cols,
                                                int64_t row_stride, int32_t group, uint8_t* codes, uint16_t* scales,
                                                uint8_t* zeros, void* hip_stream);
@@ -394,9 +396,13 @@ colibri_moe_status_t colibri_moe_int4_pack(const colibri_moe_int4_t* m, const ui
  * x bf16, y bf16 or fp32 (y_dtype), dense; y may overlap neither x, ids, weights
  * nor packed (INVALID_ARG). An id
  * outside 0..n_experts-1 marks a slot without an expert: its row of y is 0, and
- * it adds nothing to a weighted sum. Ids may repeat. Weights enter the products unrounded; sums are fp32, in
- * an order that the call's sizes and ids decide (the same call gives the same
- * bits), and no row's values reach another row. x must be below
+ * it adds nothing to a weighted sum. Ids may repeat. Weights enter the products
+ * unrounded; sums are fp32, in an order that the call's sizes and ids decide (the
+ * same call gives the same bits), and no row's values reach another row. A group
+ * adds s * (sum (16 + q) x - (16 + z) sum x), whose parts are larger than their
+ * difference: the rms error of an fp32 y is 0.6 to 3.3e-7 of y's rms for normal
+ * values (a library's fp32 product of the same: 0.8 to 5.2e-7), and 5 to 9e-7 where
+ * a few channels of x are 1000 times the others (4.5 to 6e-7). x must be below
  * 2^115 in magnitude; a row with an infinity or NaN gives NaN. T >= 0 (0:
  * nothing to do), k 1..8, T * k <= COLIBRI_MOE_INT4_ROWS (TOO_LARGE). packed
  * and x 16-byte, ids, weights and fp32 y 4-byte, bf16 y 2-byte aligned.

@@ -22,8 +22,11 @@
 //     lie in one group; its scales and zero points are a dword per row and group.
 //   * The waves of a workgroup split its units and add their totals through LDS in
 //     wave order: the result does not depend on what else runs.
-// One token x 4096 x 4096: 4.2 us with the launch, of which 1.6 are the weights' 9 MB;
-// 16 tokens on 8 experts of 28672 x 4096 (SwiGLU, 4 rows each): 87 us, 5.6 TB/s.
+// One token x 4096 x 4096: 4.9 us with the launch, of which 1.6 are the weights' 9 MB;
+// 16 tokens on 8 experts of 28672 x 4096 (SwiGLU, 4 rows each): 86 us, 5.7 TB/s.
+// All times here are a call's in a replayed graph of such calls, three sets of inputs
+// in turn. Times of two choices are of one card at the time the choice was made; other
+// cards, and later changes to what both share, move them by up to a tenth.
 #include "common.hpp"
 
 namespace cmoe {
@@ -352,8 +355,8 @@ __device__ __forceinline__ int total_col(int v) { return v & 15; }
 // and the wave turns them in its own 4 KiB of LDS per 16 rows: piece p of row r is at
 // place p ^ r of its row, so that neither side has bank conflicts. Rows of the 16
 // that were not loaded hold anything: a row of the products depends on its own
-// row of x. (4096 x 4096, 12 rows: 7.9 -> 5.0 us, 64: 20.2 -> 8.3; 14336 x 4096, 128 rows:
-// 69.5 -> 29.4.)
+// row of x. (4096 x 4096, 12 rows: 7.9 us in the operands' order, 5.4 so; 64: 20.2, 9.4;
+// 14336 x 4096, 128 rows: 69.5, 35.8.)
 template <int L, int NT, int RT, int MG, int Q>
 struct Stream {
     static_assert(NT == 1 || L == 4, "rows");
@@ -714,8 +717,10 @@ hipError_t launch_int4_linear(const Int4Args& a, int cus, hipStream_t s)
     const int A = a.T * a.k;
     // The rows that passes hold: with ids, the mean of the chosen experts' (if all
     // choose alike), in eighths. Fewer rows per pass need fewer loads of x, but
-    // an expert of more is read again: passes of 4 up to 1.6 rows, of 8 up to 4.5, of
-    // 16 up to 12. A weighted sum stays at 16, whose tokens' sums take the LDS.
+    // an expert of more is read again, from a cache: passes of 4 up to 1.6 rows, of 8 up to 4.5, of
+    // 16 up to 12. A weighted sum stays at 16, whose tokens' sums take the LDS. Ids that
+    // crowd get the passes of the mean (64 tokens, k = 2, 1536 x 2048, 128 experts, passes of 4:
+    // 83 experts in use 35.4 us, 32 20.1, 8 16.9, 2 13.0).
     const int rows = !a.ids ? a.T * 8 : a.T <= 4 ? 8 : std::min(a.T * 8, A * 8 / std::min(a.E, A));
     const int few = a.ids ? 13 : 32, some = a.ids ? 36 : 64, more = a.ids ? 96 : 128;
     if (a.w) {

@@ -18,7 +18,9 @@
 // once and a reduction over a token is four steps within the row. Instruction
 // issue bounds it: 16384 tokens, 256 experts, 8 of them in 4 of 8 groups took
 // 30 us with a wave per token and take 13 us so (reading the logits: 3.3 us); 2047
-// tokens of 128 experts 4.2 us both ways, 32 of 8 2.6 us.
+// tokens of 128 experts 3.9 us, 32 of 8 3.0 us. In a layer's router, whose waves that have
+// no token of their own repeat the last one's selection, a rule adds 4 us to a
+// call of 1 to 1024 tokens on 128 experts (11.6 -> 15.4 us for one token), 1.6 at 4096.
 #pragma once
 
 #include "topk.hpp"
